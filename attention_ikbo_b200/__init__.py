@@ -24,6 +24,11 @@ Operations ("ROCS: Request-Oriented Compute Sharing ...", arXiv:2607.27744):
   * :func:`rocs_chain_split_forward` / :func:`chain_split_forward` -- the chain with the projection
     split over the IKBO decomposition (request term once per request, W_q folded with W_CC by
     :func:`rocs_chain_prepare_weights`), so Y^C is never written.
+Request histories kept between calls (no counterpart in the paper):
+  * :func:`rocs_qk_norm_rope_forward` -- per-head norm of queries and keys with the position rotation in the
+    same pass (table: :func:`rocs_rope_table`).
+  * :func:`rocs_cache_append` / :func:`rocs_cache_read` -- keys and values into a paged 4-bit cache
+    (:class:`CacheQ4`), keys rotated on the way, and back as dense bf16.
 """
 from ._binding import (  # noqa: F401
     ROCS_BF16,
@@ -55,4 +60,11 @@ from ._binding import (  # noqa: F401
     rocs_proj_forward,
     rocs_read_status,
     STATUS_NAMES,
+)
+from ._history import (  # noqa: F401
+    CacheQ4,
+    rocs_cache_append,
+    rocs_cache_read,
+    rocs_qk_norm_rope_forward,
+    rocs_rope_table,
 )

@@ -1,0 +1,59 @@
+// history.h -- parameters and launchers of the history-cache kernels: per-head norm and rotation, the paged 4-bit
+// cache's append and read, and the attention over it.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace rocs {
+
+// ---------------------------------------------------------------- per-head norm + rotation
+struct NormRopeSide {
+  const void* x;
+  void* out;
+  const int32_t* pos;  // [n], or null without rotation
+  const float* gamma;  // [dh] or null
+  const float* beta;   // [dh] or null
+  int64_t ld_x, ld_out;
+  int n, heads, groups;  // groups: warps per token
+};
+struct NormRopeParams {
+  NormRopeSide side[2];  // queries, keys
+  int64_t warps0, warps;  // warps of side 0, of both
+  const float* rope;      // [max_pos, rot] or null
+  int max_pos, rot, interleaved, norm;
+  float eps;
+  WsHeader* ws;
+};
+cudaError_t launch_norm_rope(const NormRopeParams& p, int dh, bool f32, int unroll, cudaStream_t st);
+// rows of one head that a warp of the kernels below handles at a time, and how many such steps are unrolled
+inline int rows_per_warp(int64_t dh) { return (int)(256 / dh); }
+inline int unroll_for(int64_t heads, int64_t dh) {
+  const int64_t steps = (heads + rows_per_warp(dh) - 1) / rows_per_warp(dh);
+  return steps >= 4 ? 4 : steps >= 2 ? 2 : 1;
+}
+cudaError_t launch_rope_table(float* table, int64_t max_pos, int rot, double base, cudaStream_t st);
+
+// ---------------------------------------------------------------- the paged 4-bit cache
+// codes [pages, heads, page, dh/2] bytes, scale [pages, heads, page, 2] bf16 (step, minimum)
+struct CacheQ4 {
+  uint8_t* codes[2];          // K, V
+  __nv_bfloat162* scale[2];
+  int pages, page_log2, heads;
+};
+struct CacheMoveParams {  // append and read
+  CacheQ4 c;
+  void* x[2];              // append: k, v in;  read: k, v out
+  int64_t ld[2];           // token stride in elements
+  const int32_t* tok_off;  // [R+1]
+  const int32_t* base;     // [R]
+  const int32_t* table;    // [R, max_pages]
+  const int32_t* pos;      // [T] or null
+  const float* rope;
+  int R, max_pages, max_pos, rot, interleaved, groups;
+  int64_t warps;           // T * 2 * groups
+  WsHeader* ws;
+};
+cudaError_t launch_cache_append(const CacheMoveParams& p, int dh, bool f32, int unroll, cudaStream_t st);
+cudaError_t launch_cache_read(const CacheMoveParams& p, int dh, int unroll, cudaStream_t st);
+
+}  // namespace rocs

@@ -1,0 +1,244 @@
+// history_abi.cu -- host side of the history-cache entry points: argument checks and launches.
+#include <cmath>
+#include <cstring>
+
+#include "history.h"
+
+namespace rocs {
+int sm_count_ext();
+int check_csr_ext(const int32_t* off, int64_t R, int64_t* total);
+void set_last_launches(int n);
+}  // namespace rocs
+
+using namespace rocs;
+
+namespace {
+
+inline bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int rope_validate(const float* rope, int64_t max_pos, int64_t rot, int64_t dh) {
+  if (!rope) return ROCS_OK;
+  if (!al(rope, 16) || max_pos <= 0) return ROCS_ERR_INVALID_ARG;
+  if (rot <= 0 || rot > dh || rot % 16 || max_pos >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
+  return ROCS_OK;
+}
+
+int workspace_validate(const void* ws, size_t have, size_t need) {
+  return !ws || have < need || !al(ws, 256) ? ROCS_ERR_WORKSPACE : ROCS_OK;
+}
+
+// first and one past the last byte of n rows of `row` elements, ld elements apart
+struct Span {
+  uintptr_t lo, hi;
+};
+Span span(const void* p, int64_t n, int64_t row, int64_t ld, int64_t es) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  return {b, b + (uintptr_t)(((n - 1) * ld + row) * es)};
+}
+
+int side_validate(const rocs_norm_rope_side& s, const rocs_norm_rope_args* a) {
+  if (s.n < 0 || s.heads < 0) return ROCS_ERR_INVALID_ARG;
+  if (s.n == 0) return ROCS_OK;
+  if (s.heads == 0 || !s.x || !s.out) return ROCS_ERR_INVALID_ARG;
+  const int64_t row = s.heads * a->dh, es = a->dtype == ROCS_BF16 ? 2 : 4;
+  if (s.n >= (int64_t(1) << 31) || row >= (int64_t(1) << 24)) return ROCS_ERR_UNSUPPORTED;
+  const int64_t ldx = s.ld_x ? s.ld_x : row, ldo = s.ld_out ? s.ld_out : row;
+  if (ldx < row || ldo < row) return ROCS_ERR_INVALID_ARG;
+  if ((ldx * es) % 16 || (ldo * es) % 16 || ldx >= (int64_t(1) << 31) || ldo >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
+  if (!al(s.x, 16) || !al(s.out, 16)) return ROCS_ERR_INVALID_ARG;
+  if (a->rope && (!s.pos || !al(s.pos, 4))) return ROCS_ERR_INVALID_ARG;
+  if ((s.gamma && !al(s.gamma, 16)) || (s.beta && !al(s.beta, 16))) return ROCS_ERR_INVALID_ARG;
+  return ROCS_OK;
+}
+
+// an output may be its own side's input in place; nothing else may overlap an output
+int overlap_validate(const rocs_norm_rope_args* a) {
+  const rocs_norm_rope_side* s[2] = {&a->q, &a->k};
+  const int64_t es = a->dtype == ROCS_BF16 ? 2 : 4;
+  for (int o = 0; o < 2; ++o) {
+    if (s[o]->n == 0) continue;
+    const int64_t row = s[o]->heads * a->dh, ldo = s[o]->ld_out ? s[o]->ld_out : row;
+    const Span out = span(s[o]->out, s[o]->n, row, ldo, es);
+    for (int i = 0; i < 4; ++i) {  // 0, 1: inputs; 2, 3: outputs
+      const rocs_norm_rope_side* t = s[i & 1];
+      if (t->n == 0 || (i >= 2 && (i & 1) == o)) continue;
+      const int64_t rowt = t->heads * a->dh, ldt = (i < 2 ? t->ld_x : t->ld_out) ? (i < 2 ? t->ld_x : t->ld_out) : rowt;
+      const void* pt = i < 2 ? t->x : t->out;
+      if (i < 2 && (i & 1) == o && pt == s[o]->out && ldt == ldo) continue;
+      const Span q = span(pt, t->n, rowt, ldt, es);
+      if (out.hi <= q.lo || q.hi <= out.lo) continue;
+      // rows of one wider buffer side by side: same stride, columns apart
+      if (ldt == ldo) {
+        const int64_t ldb = ldo * es, d = (int64_t)(q.lo > out.lo ? q.lo - out.lo : out.lo - q.lo) % ldb;
+        const int64_t first = q.lo > out.lo ? row * es : rowt * es, second = q.lo > out.lo ? rowt * es : row * es;
+        if (d >= first && d + second <= ldb) continue;
+      }
+      return ROCS_ERR_INVALID_ARG;
+    }
+  }
+  return ROCS_OK;
+}
+
+int norm_rope_validate(const rocs_norm_rope_args* a) {
+  if (!a || a->dh <= 0) return ROCS_ERR_INVALID_ARG;
+  if (a->dtype != ROCS_F32 && a->dtype != ROCS_BF16) return ROCS_ERR_INVALID_ARG;
+  if (a->norm < ROCS_NORM_NONE || a->norm > ROCS_NORM_RMS) return ROCS_ERR_INVALID_ARG;
+  if (!(a->eps >= 0.0f) || !std::isfinite(a->eps)) return ROCS_ERR_INVALID_ARG;
+  if (a->dh != 64 && a->dh != 128) return ROCS_ERR_UNSUPPORTED;
+  int rc = rope_validate(a->rope, a->max_pos, a->rot, a->dh);
+  if (rc || (rc = side_validate(a->q, a)) || (rc = side_validate(a->k, a))) return rc;
+  return overlap_validate(a);
+}
+
+int cache_validate(const rocs_cache_q4& c) {
+  if (c.pages < 0 || c.page <= 0 || c.heads <= 0 || c.dh <= 0) return ROCS_ERR_INVALID_ARG;
+  if (c.dh != 64 && c.dh != 128) return ROCS_ERR_UNSUPPORTED;
+  if (c.page != 16 && c.page != 32 && c.page != 64 && c.page != 128) return ROCS_ERR_UNSUPPORTED;
+  if (c.pages >= (int64_t(1) << 31) || c.heads >= (int64_t(1) << 16) || c.pages * c.heads * c.page >= (int64_t(1) << 40))
+    return ROCS_ERR_UNSUPPORTED;
+  const void* ptrs[] = {c.k_codes, c.v_codes, c.k_scale, c.v_scale};
+  for (const void* p : ptrs)
+    if ((c.pages > 0 && !p) || !al(p, 16)) return ROCS_ERR_INVALID_ARG;
+  return ROCS_OK;
+}
+CacheQ4 cache_of(const rocs_cache_q4& c) {
+  CacheQ4 q;
+  q.codes[0] = static_cast<uint8_t*>(c.k_codes);
+  q.codes[1] = static_cast<uint8_t*>(c.v_codes);
+  q.scale[0] = static_cast<__nv_bfloat162*>(c.k_scale);
+  q.scale[1] = static_cast<__nv_bfloat162*>(c.v_scale);
+  q.pages = (int)c.pages;
+  q.heads = (int)c.heads;
+  q.page_log2 = c.page == 16 ? 4 : c.page == 32 ? 5 : c.page == 64 ? 6 : 7;
+  return q;
+}
+
+int move_validate(const rocs_cache_move_args* a, bool append, int64_t* T) {
+  if (!a) return ROCS_ERR_INVALID_ARG;
+  int rc = cache_validate(a->cache);
+  if (rc) return rc;
+  if (a->R < 0 || a->max_pages < 0) return ROCS_ERR_INVALID_ARG;
+  if (a->R >= (int64_t(1) << 28) || a->max_pages >= (int64_t(1) << 27)) return ROCS_ERR_UNSUPPORTED;
+  if (a->dtype != ROCS_F32 && a->dtype != ROCS_BF16) return ROCS_ERR_INVALID_ARG;
+  if (!append && a->dtype != ROCS_BF16) return ROCS_ERR_UNSUPPORTED;
+  if ((rc = check_csr_ext(a->tok_off_host, a->R, T))) return rc;
+  if (*T == 0) return ROCS_OK;
+  if (!a->tok_off_dev || !a->base || !a->k || !a->v || (a->max_pages > 0 && !a->page_table)) return ROCS_ERR_INVALID_ARG;
+  if (!al(a->k, 16) || !al(a->v, 16) || !al(a->base, 4) || !al(a->page_table, 4) || !al(a->pos, 4)) return ROCS_ERR_INVALID_ARG;
+  const int64_t row = a->cache.heads * a->cache.dh, es = a->dtype == ROCS_BF16 ? 2 : 4;
+  for (int64_t ld : {a->k_ld, a->v_ld}) {
+    if (ld != 0 && ld < row) return ROCS_ERR_INVALID_ARG;
+    if ((ld * es) % 16 || ld >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
+  }
+  return append ? rope_validate(a->rope, a->max_pos, a->rot, a->cache.dh) : ROCS_OK;
+}
+
+int cache_move(const rocs_cache_move_args* a, bool append, cudaStream_t st) {
+  int64_t T = 0;
+  int rc = move_validate(a, append, &T);
+  if (rc || (rc = workspace_validate(a->workspace, a->workspace_bytes, sizeof(WsHeader)))) return rc;
+  CacheMoveParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = cache_of(a->cache);
+  const int64_t row = a->cache.heads * a->cache.dh;
+  p.x[0] = const_cast<void*>(a->k);
+  p.x[1] = const_cast<void*>(a->v);
+  p.ld[0] = a->k_ld ? a->k_ld : row;
+  p.ld[1] = a->v_ld ? a->v_ld : row;
+  p.tok_off = a->tok_off_dev;
+  p.base = a->base;
+  p.table = a->page_table;
+  p.pos = a->pos;
+  p.rope = append ? a->rope : nullptr;
+  p.R = (int)a->R;
+  p.max_pages = (int)a->max_pages;
+  p.max_pos = (int)a->max_pos;
+  p.rot = (int)a->rot;
+  p.interleaved = a->interleaved != 0;
+  p.ws = static_cast<WsHeader*>(a->workspace);
+  const int unroll = unroll_for(a->cache.heads, a->cache.dh), per = unroll * rows_per_warp(a->cache.dh);
+  p.groups = (int)((a->cache.heads + per - 1) / per);
+  p.warps = T * 2 * p.groups;
+  if (p.warps >= (int64_t(1) << 33)) return ROCS_ERR_UNSUPPORTED;
+  if (cudaMemsetAsync(p.ws, 0, sizeof(WsHeader), st) != cudaSuccess) return ROCS_ERR_CUDA;
+  if (T > 0) {
+    const cudaError_t e = append ? launch_cache_append(p, (int)a->cache.dh, a->dtype == ROCS_F32, unroll, st)
+                                 : launch_cache_read(p, (int)a->cache.dh, unroll, st);
+    if (e != cudaSuccess) return ROCS_ERR_CUDA;
+  }
+  set_last_launches(T > 0 ? 1 : 0);
+  return ROCS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rocs_qk_norm_rope_workspace_size(const rocs_norm_rope_args* a) {
+  return norm_rope_validate(a) == ROCS_OK ? sizeof(WsHeader) : 0;
+}
+
+int rocs_qk_norm_rope_forward(const rocs_norm_rope_args* a, rocs_stream_t stream) {
+  int rc = norm_rope_validate(a);
+  if (rc || (rc = workspace_validate(a->workspace, a->workspace_bytes, sizeof(WsHeader)))) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  NormRopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  const int64_t heads = a->q.n == 0 ? a->k.heads : a->k.n == 0 ? a->q.heads : a->q.heads > a->k.heads ? a->q.heads : a->k.heads;
+  const int unroll = unroll_for(heads, a->dh), per = unroll * rows_per_warp(a->dh);
+  const rocs_norm_rope_side* s[2] = {&a->q, &a->k};
+  for (int i = 0; i < 2; ++i) {
+    const int64_t row = s[i]->heads * a->dh;
+    p.side[i].x = s[i]->x;
+    p.side[i].out = s[i]->out;
+    p.side[i].pos = s[i]->pos;
+    p.side[i].gamma = s[i]->gamma;
+    p.side[i].beta = s[i]->beta;
+    p.side[i].ld_x = s[i]->ld_x ? s[i]->ld_x : row;
+    p.side[i].ld_out = s[i]->ld_out ? s[i]->ld_out : row;
+    p.side[i].n = (int)s[i]->n;
+    p.side[i].heads = (int)s[i]->heads;
+    p.side[i].groups = (int)((s[i]->heads + per - 1) / per);
+    p.warps += s[i]->n * p.side[i].groups;
+    if (i == 0) p.warps0 = p.warps;
+  }
+  if (p.warps >= (int64_t(1) << 33)) return ROCS_ERR_UNSUPPORTED;
+  p.rope = a->rope;
+  p.max_pos = (int)a->max_pos;
+  p.rot = (int)a->rot;
+  p.interleaved = a->interleaved != 0;
+  p.norm = a->norm;
+  p.eps = a->eps;
+  p.ws = static_cast<WsHeader*>(a->workspace);
+  if (cudaMemsetAsync(p.ws, 0, sizeof(WsHeader), st) != cudaSuccess) return ROCS_ERR_CUDA;
+  if (p.warps > 0 && launch_norm_rope(p, (int)a->dh, a->dtype == ROCS_F32, unroll, st) != cudaSuccess) return ROCS_ERR_CUDA;
+  set_last_launches(p.warps > 0 ? 1 : 0);
+  return ROCS_OK;
+}
+
+int rocs_rope_table(float* table, int64_t max_pos, int64_t rot, double base, rocs_stream_t stream) {
+  if (max_pos < 0 || rot <= 0 || !(base > 1.0) || !std::isfinite(base)) return ROCS_ERR_INVALID_ARG;
+  if (rot % 16 || rot > 128 || max_pos >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
+  if (max_pos == 0) {
+    set_last_launches(0);
+    return ROCS_OK;
+  }
+  if (!table || !al(table, 16)) return ROCS_ERR_INVALID_ARG;
+  if (launch_rope_table(table, max_pos, (int)rot, base, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return ROCS_ERR_CUDA;
+  set_last_launches(1);
+  return ROCS_OK;
+}
+
+size_t rocs_cache_workspace_size(const rocs_cache_move_args* a) {
+  int64_t T;
+  return move_validate(a, true, &T) == ROCS_OK ? sizeof(WsHeader) : 0;
+}
+int rocs_cache_append(const rocs_cache_move_args* a, rocs_stream_t stream) {
+  return cache_move(a, true, reinterpret_cast<cudaStream_t>(stream));
+}
+int rocs_cache_read(const rocs_cache_move_args* a, rocs_stream_t stream) {
+  return cache_move(a, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

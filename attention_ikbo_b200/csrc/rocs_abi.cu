@@ -417,6 +417,8 @@ int dca_run_ext(const rocs_dca_args* a, int64_t C, int64_t T, int64_t n_units, W
 size_t dca_body_bytes_ext(int64_t R, int64_t n_units) { return dca_body(R, n_units).body; }
 int64_t dca_units_ext(const rocs_dca_args* a) { return dca_units(a); }
 void set_last_launches(int n) { g_last_launches = n; }
+int sm_count_ext() { return sm_count(); }
+int check_csr_ext(const int32_t* off, int64_t R, int64_t* total) { return check_csr(off, R, total); }
 std::atomic<uint64_t>& configured_device_mask_ref() {
   static std::atomic<uint64_t> mask{0};
   return mask;

@@ -441,6 +441,115 @@ ROCS_API int rocs_dca_forward_host(const rocs_dca_args* args, int64_t chunks, vo
                                    rocs_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * Norm of queries and keys for each head, with the position rotation in the same pass (the paper has
+ * no counterpart: its attention takes Q and K as they are)
+ *
+ *   y = Norm(x) over the dh values of one head of one token, then per pair (a, b) of channels
+ *   (a, b) -> (a c - b s, b c + a s)      c, s: cosine and sine of the token's position
+ * Two sides, queries and keys, in one launch; a side with n = 0 is skipped.
+ *   x   [n, heads, dh] in, row stride ld_x elements per token (0 = heads*dh), heads dense
+ *   out [n, heads, dh] out, row stride ld_out likewise; out == x with ld_out == ld_x works in place,
+ *       any other overlap is ROCS_ERR_INVALID_ARG
+ *   pos [n]            position of each token (needed when rope is given)
+ *   gamma, beta [dh] fp32 16-byte aligned, or NULL (1, 0); unused with ROCS_NORM_NONE
+ *   norm ROCS_NORM_NONE, _LAYER or _RMS; eps >= 0 inside the square root
+ *   rope [max_pos, rot] fp32: rot/2 cosines, then rot/2 sines of each position (rocs_rope_table);
+ *       NULL: no rotation.  The first rot channels turn: channel i with i + rot/2, or, interleaved
+ *       != 0, channel 2i with 2i + 1.  The others pass.  rot % 16 == 0, 0 < rot <= dh.
+ * dtype ROCS_BF16 or ROCS_F32 (x and out); statistics and rotation in fp32, one rounding when
+ * stored.  dh in {64, 128}; pointers 16-byte aligned, strides multiples of 16 bytes.  A position
+ * outside [0, max_pos) sets ROCS_ERR_DEVICE_INDEX in the workspace status (that token's outputs are
+ * undefined).  Workspace: 256 bytes.  One kernel launch.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+  const void* x;
+  void* out;
+  const int32_t* pos;
+  const float* gamma;
+  const float* beta;
+  int64_t n, heads, ld_x, ld_out;
+} rocs_norm_rope_side;
+typedef struct {
+  rocs_norm_rope_side q, k;
+  int64_t dh;
+  int32_t dtype; /* rocs_dtype */
+  int32_t norm;  /* rocs_norm */
+  float eps;
+  const float* rope;
+  int64_t max_pos, rot;
+  int32_t interleaved;
+  void* workspace;
+  size_t workspace_bytes;
+} rocs_norm_rope_args;
+
+ROCS_API size_t rocs_qk_norm_rope_workspace_size(const rocs_norm_rope_args* args);
+ROCS_API int rocs_qk_norm_rope_forward(const rocs_norm_rope_args* args, rocs_stream_t stream);
+
+/* Fills table [max_pos, rot] for the rotation: the angle of pair i at position p is p * base^(-2i/rot),
+ * computed in 64 bits.  base > 1 and finite; rot as above; max_pos >= 0.  One launch. */
+ROCS_API int rocs_rope_table(float* table, int64_t max_pos, int64_t rot, double base, rocs_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Paged 4-bit cache of request histories (no counterpart in the paper, which rebuilds K and V with
+ * every batch): K and V of each request kept from call to call, `page` tokens to a page.
+ *   k_codes, v_codes [pages, heads, page, dh/2] bytes     k_scale, v_scale [pages, heads, page, 2] bf16
+ * One row (a head of a token) holds dh codes c in 0..15 with its step and minimum (in this order) and
+ * stands for minimum + step * c, where
+ *   minimum = bf16(min x),  step = bf16((max x - min x) / 15),  c = clamp(rint((x - minimum) / step), 0, 15).
+ * In each little-endian 32-bit word of codes (8 channels) nibble i of the low half is channel 2i,
+ * nibble i of the high half channel 2i + 1.  A row with an infinity or a NaN in it, or whose range
+ * passes fp32, is held with a NaN step and minimum and reads as NaN.
+ * dh in {64, 128}; page in {16, 32, 64, 128}; pages * heads * page < 2^40; codes 16-byte and scale
+ * 16-byte aligned.
+ * Page tables: [R, max_pages] int32; token j of request r is in page table[r, j / page].  Several
+ * requests may share pages that are only read.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  void* k_scale;
+  void* v_scale;
+  int64_t pages, page, heads, dh;
+} rocs_cache_q4;
+
+/* Append: token i of request r (row tok_off[r] + i of k and v) goes to slot base[r] + i of its history;
+ * keys are rotated on the way.  Rows of the cache that no token goes to keep their contents; base is
+ * not changed (the caller adds the counts).
+ *   k, v [T, heads, dh] of `dtype` (bf16 or fp32), row strides k_ld, v_ld elements (0 = heads*dh);
+ *       T = tok_off_host[R]; strides multiples of 16 bytes
+ *   base [R] int32     tokens of each request that the cache holds already
+ *   rope, max_pos, rot, interleaved: as in rocs_qk_norm_rope_forward (NULL: keys as they are)
+ *   pos [T] positions of the tokens, or NULL: a token's slot is its position
+ * A slot past the page table, a page outside [0, pages) or a position outside [0, max_pos) sets
+ * ROCS_ERR_DEVICE_INDEX and leaves that token out.  Two tokens must not go to one place.
+ * rocs_cache_read: the reverse, rows of the cache as bf16 values (rounded once) in k, v (outputs; dtype
+ * must be ROCS_BF16; rope and pos are ignored): what rocs_dca_forward reads.  A token whose place is
+ * bad reads as zeros and sets ROCS_ERR_DEVICE_INDEX.
+ * Workspace: 256 bytes.  One kernel launch each. */
+typedef struct {
+  rocs_cache_q4 cache;
+  int64_t R, max_pages;
+  const int32_t* tok_off_dev;  /* [R+1] */
+  const int32_t* tok_off_host; /* [R+1] */
+  const int32_t* base;         /* [R], device */
+  const int32_t* page_table;   /* [R, max_pages], device */
+  const void* k;
+  const void* v;
+  int64_t k_ld, v_ld;
+  int32_t dtype; /* rocs_dtype of k and v */
+  const float* rope;
+  int64_t max_pos, rot;
+  int32_t interleaved;
+  const int32_t* pos;
+  void* workspace;
+  size_t workspace_bytes;
+} rocs_cache_move_args;
+
+ROCS_API size_t rocs_cache_workspace_size(const rocs_cache_move_args* args);
+ROCS_API int rocs_cache_append(const rocs_cache_move_args* args, rocs_stream_t stream);
+ROCS_API int rocs_cache_read(const rocs_cache_move_args* args, rocs_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Status and introspection
  * ---------------------------------------------------------------------------------- */
 
