@@ -29,6 +29,8 @@ Request histories kept between calls (no counterpart in the paper):
     same pass (table: :func:`rocs_rope_table`).
   * :func:`rocs_cache_append` / :func:`rocs_cache_read` -- keys and values into a paged 4-bit cache
     (:class:`CacheQ4`), keys rotated on the way, and back as dense bf16.
+  * :func:`rocs_dca_cache_forward` -- IKBO-DCA over that cache, read in place (shared key heads, a key limit for
+    each candidate).
 """
 from ._binding import (  # noqa: F401
     ROCS_BF16,
@@ -65,6 +67,7 @@ from ._history import (  # noqa: F401
     CacheQ4,
     rocs_cache_append,
     rocs_cache_read,
+    rocs_dca_cache_forward,
     rocs_qk_norm_rope_forward,
     rocs_rope_table,
 )

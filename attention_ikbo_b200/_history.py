@@ -35,6 +35,13 @@ class CacheMoveArgs(ctypes.Structure):
                 ("workspace", _vp), ("workspace_bytes", _sz)]
 
 
+class DcaCacheArgs(ctypes.Structure):
+    _fields_ = [("cache", CacheQ4Args), ("R", _i64), ("q", _i64), ("H", _i64), ("max_pages", _i64), ("scale", _f32),
+                ("cand_off_dev", _vp), ("cand_off_host", _vp), ("seq_len", _vp), ("page_table", _vp), ("key_limit", _vp),
+                ("q_ptr", _vp), ("q_ld", _i64), ("o_ptr", _vp), ("lse_ptr", _vp), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
+
+
 _ready = None
 
 
@@ -44,12 +51,14 @@ def _lib():
         lib = _b.load_library()
         P = ctypes.POINTER
         for name, argt in [("rocs_qk_norm_rope_workspace_size", [P(NormRopeArgs)]),
-                           ("rocs_cache_workspace_size", [P(CacheMoveArgs)])]:
+                           ("rocs_cache_workspace_size", [P(CacheMoveArgs)]),
+                           ("rocs_dca_cache_workspace_size", [P(DcaCacheArgs)])]:
             getattr(lib, name).restype = _sz
             getattr(lib, name).argtypes = argt
         for name, argt in [("rocs_qk_norm_rope_forward", [P(NormRopeArgs), _vp]),
                            ("rocs_rope_table", [_vp, _i64, _i64, ctypes.c_double, _vp]),
-                           ("rocs_cache_append", [P(CacheMoveArgs), _vp]), ("rocs_cache_read", [P(CacheMoveArgs), _vp])]:
+                           ("rocs_cache_append", [P(CacheMoveArgs), _vp]), ("rocs_cache_read", [P(CacheMoveArgs), _vp]),
+                           ("rocs_dca_cache_forward", [P(DcaCacheArgs), _vp])]:
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = argt
         _ready = lib
@@ -276,3 +285,48 @@ def _read(k_codes, cache, tok_off, base, page_table, k, v, workspace, stream):
     _hold(stream, ws, keep[0], k, v)
     rocs_cache_read.last_workspace = ws
     return k, v
+
+
+@_on_tensor_device
+def rocs_dca_cache_forward(q_t, cache, page_table, seq_len, cand_off, q_tokens, scale, key_limit=None, o=None, lse=True,
+                           workspace=None, stream=None):
+    """IKBO-DCA over a :class:`CacheQ4`: ``q_t`` [C*q, H, dh] bf16 (tokens may lie apart, H a multiple of the cache's
+    heads), ``seq_len`` [R] int32 keys of each history, ``key_limit`` [C] int32 (optional) keys that a candidate sees.
+    Returns ``(o [C*q, H, dh], lse [C*q, H] or None)``."""
+    lib = _lib()
+    dev = q_t.device
+    off_d, off_h = _offsets(cand_off, dev)
+    R, C = len(off_h) - 1, int(off_h[-1])
+    _cuda(off_d, torch.int32, "cand_off", dev, 1)
+    c = _cache(cache, dev)
+    q_ptr, q_ld = _rows(q_t, torch.bfloat16, "q", dev, None, c.dh)
+    if q_t.shape[0] != C * q_tokens:
+        raise RocsError(1, f"q has {q_t.shape[0]} tokens, cand_off counts {C} candidates of {q_tokens}")
+    shape = tuple(q_t.shape)
+    if o is None:
+        o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _cuda(o, torch.bfloat16, "o", dev)
+    if lse is True:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    for t, want, what in ((o, shape, "o"), (lse, shape[:2], "lse")):
+        if t is not None and tuple(t.shape) != want:
+            raise RocsError(1, f"{what} has shape {tuple(t.shape)}, expected {want}")
+    if key_limit is not None and tuple(key_limit.shape) != (C,):
+        raise RocsError(1, f"key_limit must have one entry for each of {C} candidates")
+    a = DcaCacheArgs(cache=c, R=R, q=int(q_tokens), H=shape[1], max_pages=page_table.shape[1], scale=float(scale),
+                     cand_off_dev=off_d.data_ptr(), cand_off_host=off_h.ctypes.data,
+                     seq_len=_per_request(seq_len, R, "seq_len", dev), page_table=_table(page_table, R, dev),
+                     key_limit=None if key_limit is None or C == 0 else _cuda(key_limit, torch.int32, "key_limit", dev),
+                     q_ptr=q_ptr, q_ld=q_ld, o_ptr=o.data_ptr() if C else None,
+                     lse_ptr=_cuda(lse, torch.float32, "lse", dev) if lse is not None and C else None)
+    nbytes = lib.rocs_dca_cache_workspace_size(ctypes.byref(a))
+    if nbytes == 0:
+        _check(lib.rocs_dca_cache_forward(ctypes.byref(a), _stream(stream)), "rocs_dca_cache_forward")
+    ws = _workspace(nbytes, dev, workspace)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _check(lib.rocs_dca_cache_forward(ctypes.byref(a), _stream(stream)), "rocs_dca_cache_forward")
+    _hold(stream, ws, off_d, o, lse)
+    rocs_dca_cache_forward.last_workspace = ws
+    return o, lse

@@ -56,4 +56,28 @@ struct CacheMoveParams {  // append and read
 cudaError_t launch_cache_append(const CacheMoveParams& p, int dh, bool f32, int unroll, cudaStream_t st);
 cudaError_t launch_cache_read(const CacheMoveParams& p, int dh, int unroll, cudaStream_t st);
 
+// ---------------------------------------------------------------- attention over the cache
+struct CacheAttnParams {
+  CacheQ4 c;
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  float* lse;                // or null
+  const int32_t* cand_off;   // [R+1]
+  const int32_t* seq_len;    // [R]
+  const int32_t* table;      // [R, max_pages]
+  const int32_t* key_limit;  // [C] or null
+  int64_t q_ld;              // elements from one query token to the next
+  int R, C, q_tokens, H, G;  // G: query heads to a key head
+  int max_pages, capacity;   // capacity: slots that a row of the page table reaches
+  int rows_lo, rows_hi;      // requests with rows_lo < rows (of one key head) <= rows_hi are this launch's
+  float scale_log2;          // softmax scale * log2(e)
+  float* part;               // partial results, two per CTA
+  int* cnt;                  // [CTAs], zeroed before the launch
+  WsHeader* ws;
+};
+constexpr int kFewRows = 16;   // rows of a unit of the kernel for few rows
+size_t cache_few_part_bytes(int dh);
+int cache_few_grid(int sms);
+cudaError_t launch_cache_few(const CacheAttnParams& p, int dh, int grid, cudaStream_t st);
+
 }  // namespace rocs

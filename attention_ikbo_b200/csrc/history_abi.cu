@@ -170,9 +170,100 @@ int cache_move(const rocs_cache_move_args* a, bool append, cudaStream_t st) {
   return ROCS_OK;
 }
 
+// ---------------------------------------------------------------- attention over the cache
+inline size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
+
+// What a call needs: which kernels run (by the rows of a key head that the requests have), and the workspace
+// [WsHeader][counters][partial results], the first two zeroed before every call.
+struct AttnPlan {
+  int64_t C = 0;
+  bool few = false;
+  int grid_few = 0;
+  size_t zero = 0, bytes = 0;
+};
+
+int attn_validate(const rocs_dca_cache_args* a, AttnPlan* pl) {
+  if (!a) return ROCS_ERR_INVALID_ARG;
+  int rc = cache_validate(a->cache);
+  if (rc) return rc;
+  if (a->R < 0 || a->q <= 0 || a->H <= 0 || a->max_pages < 0) return ROCS_ERR_INVALID_ARG;
+  if (a->H % a->cache.heads) return ROCS_ERR_INVALID_ARG;
+  if (!std::isfinite(a->scale) || a->scale < 0.0f) return ROCS_ERR_INVALID_ARG;
+  if (a->R >= (int64_t(1) << 28) || a->q >= (int64_t(1) << 20) || a->H >= (int64_t(1) << 16) ||
+      a->max_pages * a->cache.page >= (int64_t(1) << 30))
+    return ROCS_ERR_UNSUPPORTED;
+  if ((rc = check_csr_ext(a->cand_off_host, a->R, &pl->C))) return rc;
+  if (pl->C * a->q * a->H >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
+  if (pl->C > 0) {
+    if (!a->cand_off_dev || !a->seq_len || !a->q_ptr || !a->o_ptr || (a->max_pages > 0 && !a->page_table))
+      return ROCS_ERR_INVALID_ARG;
+    if (!al(a->q_ptr, 16) || !al(a->o_ptr, 16) || !al(a->lse_ptr, 4) || !al(a->cand_off_dev, 4) || !al(a->seq_len, 4) ||
+        !al(a->page_table, 4) || !al(a->key_limit, 4))
+      return ROCS_ERR_INVALID_ARG;
+    const int64_t row = a->H * a->cache.dh;
+    if (a->q_ld != 0 && a->q_ld < row) return ROCS_ERR_INVALID_ARG;
+    if (a->q_ld % 8 || a->q_ld >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
+    pl->few = true;
+  }
+  pl->zero = sizeof(WsHeader);
+  size_t part = 0;
+  if (pl->few) {
+    pl->grid_few = cache_few_grid(sm_count_ext());
+    pl->zero += a256(sizeof(int) * (size_t)pl->grid_few);
+    part = 2 * (size_t)pl->grid_few * cache_few_part_bytes((int)a->cache.dh);
+  }
+  pl->bytes = pl->zero + part;
+  return ROCS_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t rocs_dca_cache_workspace_size(const rocs_dca_cache_args* a) {
+  AttnPlan pl;
+  return attn_validate(a, &pl) == ROCS_OK ? pl.bytes : 0;
+}
+
+int rocs_dca_cache_forward(const rocs_dca_cache_args* a, rocs_stream_t stream) {
+  AttnPlan pl;
+  int rc = attn_validate(a, &pl);
+  if (rc || (rc = workspace_validate(a->workspace, a->workspace_bytes, pl.bytes))) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+  if (cudaMemsetAsync(ws, 0, pl.zero, st) != cudaSuccess) return ROCS_ERR_CUDA;
+  CacheAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = cache_of(a->cache);
+  p.q = static_cast<const __nv_bfloat16*>(a->q_ptr);
+  p.o = static_cast<__nv_bfloat16*>(a->o_ptr);
+  p.lse = a->lse_ptr;
+  p.cand_off = a->cand_off_dev;
+  p.seq_len = a->seq_len;
+  p.table = a->page_table;
+  p.key_limit = a->key_limit;
+  p.q_ld = a->q_ld ? a->q_ld : a->H * a->cache.dh;
+  p.R = (int)a->R;
+  p.C = (int)pl.C;
+  p.q_tokens = (int)a->q;
+  p.H = (int)a->H;
+  p.G = (int)(a->H / a->cache.heads);
+  p.max_pages = (int)a->max_pages;
+  p.capacity = a->cache.pages > 0 ? (int)(a->max_pages * a->cache.page) : 0;
+  p.scale_log2 = a->scale * 1.4426950408889634f;
+  p.ws = reinterpret_cast<WsHeader*>(ws);
+  p.part = reinterpret_cast<float*>(ws + pl.zero);
+  int launches = 0;
+  if (pl.few) {
+    p.rows_lo = 0;
+    p.rows_hi = 0x7fffffff;
+    p.cnt = reinterpret_cast<int*>(ws + sizeof(WsHeader));
+    if (launch_cache_few(p, (int)a->cache.dh, pl.grid_few, st) != cudaSuccess) return ROCS_ERR_CUDA;
+    ++launches;
+  }
+  set_last_launches(launches);
+  return ROCS_OK;
+}
 
 size_t rocs_qk_norm_rope_workspace_size(const rocs_norm_rope_args* a) {
   return norm_rope_validate(a) == ROCS_OK ? sizeof(WsHeader) : 0;

@@ -549,6 +549,43 @@ ROCS_API size_t rocs_cache_workspace_size(const rocs_cache_move_args* args);
 ROCS_API int rocs_cache_append(const rocs_cache_move_args* args, rocs_stream_t stream);
 ROCS_API int rocs_cache_read(const rocs_cache_move_args* args, rocs_stream_t stream);
 
+/* IKBO-DCA over the cache: every candidate's query tokens attend to the history of their request,
+ * read in place.
+ *   q_ptr  [C*q, H, dh] bf16   query tokens, row stride q_ld elements (0 = H*dh; a multiple of 8), heads
+ *                              dense; H is a multiple of cache.heads: query head h reads key head
+ *                              h / (H / cache.heads)
+ *   seq_len [R] int32, device  keys of each history (read on the device: they may change between
+ *                              replays of a captured call)
+ *   page_table [R, max_pages]  as above; entries past a history are not read
+ *   key_limit [C] int32, device, or NULL   candidate i sees keys 0 ... key_limit[i] - 1 of its history
+ *                              only; a limit above its length means all, one below 1 none
+ *   o_ptr  [C*q, H, dh] bf16, lse_ptr [C*q, H] fp32 or NULL: as in rocs_dca_forward; O = 0 and LSE =
+ *                              -inf where a candidate sees no key
+ * Scores are exact up to fp32 sums: codes are exact in bf16, steps and minima enter in fp32.  What a
+ * masked row of the cache holds does not matter; a visible row that is held as NaN makes the result
+ * NaN.  scale >= 0 and finite.  A length outside [0, max_pages * page] is cut to that range, a page
+ * outside [0, pages) is replaced by page 0, and either sets ROCS_ERR_DEVICE_INDEX.  C*q*H < 2^31.
+ * The workspace size depends on the current device's SM count. */
+typedef struct {
+  rocs_cache_q4 cache;
+  int64_t R, q, H, max_pages;
+  float scale;
+  const int32_t* cand_off_dev;  /* [R+1] */
+  const int32_t* cand_off_host; /* [R+1] */
+  const int32_t* seq_len;
+  const int32_t* page_table;
+  const int32_t* key_limit;
+  const void* q_ptr;
+  int64_t q_ld;
+  void* o_ptr;
+  float* lse_ptr;
+  void* workspace;
+  size_t workspace_bytes;
+} rocs_dca_cache_args;
+
+ROCS_API size_t rocs_dca_cache_workspace_size(const rocs_dca_cache_args* args);
+ROCS_API int rocs_dca_cache_forward(const rocs_dca_cache_args* args, rocs_stream_t stream);
+
 /* ------------------------------------------------------------------------------------
  * Status and introspection
  * ---------------------------------------------------------------------------------- */

@@ -112,6 +112,41 @@ def test_cache_refusals(lib):
     assert lib.rocs_cache_workspace_size(P(args(off=(0, 3, 2)))) == 0
 
 
+def test_cache_attention_refusals(lib):
+    import attention_ikbo_b200._history as m
+
+    def args(off=(0, 3, 5), cache=None, **kw):
+        off = np.asarray(off, np.int32)
+        a = dict(cache=cache or _cache_args(m), R=len(off) - 1, q=1, H=4, max_pages=4, scale=0.1, cand_off_dev=FAKE,
+                 cand_off_host=off.ctypes.data, seq_len=FAKE, page_table=FAKE, q_ptr=FAKE, o_ptr=FAKE, workspace=FAKE,
+                 workspace_bytes=1 << 40)
+        a.update(kw)
+        x = m.DcaCacheArgs(**a)
+        x.keep = off
+        return x
+
+    f, size = lib.rocs_dca_cache_forward, lib.rocs_dca_cache_workspace_size
+    for kw, code in BAD_CACHES:
+        a = args(cache=_cache_args(m, **kw), H=max(4, 2 * kw.get("heads", 2)))
+        assert f(P(a), None) == code and size(P(a)) == 0, kw
+    for kw, code in [({"off": (0, 3, 2)}, 2), ({"off": (1, 3, 5)}, 2), ({"cand_off_host": None}, 1), ({"cand_off_dev": None}, 1),
+                     ({"seq_len": None}, 1), ({"page_table": None}, 1), ({"q_ptr": None}, 1), ({"o_ptr": None}, 1),
+                     ({"q_ptr": FAKE + 8}, 1), ({"o_ptr": FAKE + 2}, 1), ({"lse_ptr": FAKE + 2}, 1), ({"key_limit": FAKE + 1}, 1),
+                     ({"seq_len": FAKE + 2}, 1), ({"H": 5}, 1), ({"H": 0}, 1), ({"q": 0}, 1), ({"R": -1}, 1), ({"max_pages": -1}, 1),
+                     ({"max_pages": 1 << 26}, 3), ({"q": 1 << 20}, 3), ({"H": 1 << 16}, 3), ({"q": 1 << 19, "H": 1 << 15}, 3),
+                     ({"scale": -1.0}, 1), ({"scale": float("nan")}, 1), ({"scale": float("inf")}, 1), ({"q_ld": 64}, 1),
+                     ({"q_ld": 260}, 3), ({"q_ld": 1 << 31}, 3)]:
+        assert f(P(args(**kw)), None) == code, kw
+        assert size(P(args(**kw))) == 0, kw
+    need = size(P(args()))
+    assert need > 256 and need % 256 == 0
+    for kw in ({"workspace": None}, {"workspace_bytes": need - 1}, {"workspace": FAKE + 16}):
+        assert f(P(args(**kw)), None) == 6, kw
+    assert f(None, None) == 1
+    # nothing to compute: pointers are not needed
+    assert size(P(args(off=(0, 0), q_ptr=None, o_ptr=None, seq_len=None, page_table=None))) == 256
+
+
 def test_binding_refuses_host_tensors():
     import attention_ikbo_b200 as m
 
