@@ -51,14 +51,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// pair i of a word as bf16 (16 + low, 16 + high): the nibble moved to the top mantissa bits under the exponent of 16
-template <int I>
-__device__ __forceinline__ uint32_t pair16(uint32_t w) {
-  const uint32_t s = I == 0 ? w << 3 : I == 1 ? w >> 1 : I == 2 ? w >> 5 : w >> 9;
-  return (s & 0x00780078u) | 0x41804180u;
-}
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float quad_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 1);
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
@@ -75,8 +67,8 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
   __shared__ int64_t s_sum[33], s_out[3];
   __shared__ int s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  Work<kFewRows, kKeys> w;
-  if (!w.start(p, s_sum, s_out, 2)) return;
+  Work<kKeys> w;
+  if (!w.start(p, kFewRows, s_sum, s_out, 2)) return;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * L::kStage);
   // keys of a granule's half that this lane's score columns are (and its V rows): neighbours, in an order that spreads
   // the four lanes' V rows over all banks

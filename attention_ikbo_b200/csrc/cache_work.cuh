@@ -38,8 +38,9 @@ __device__ __forceinline__ Request request_at(const CacheAttnParams& p, int r) {
   return q;
 }
 
-template <int ROWS, int KEYS>
+template <int KEYS>
 struct Work {
+  int unit_rows;                      // rows of a chunk
   int r, head, chunk, chunks, steps;  // request, key head, chunk of rows, chunks and steps of the request's units
   Request q;
   int64_t pos, end, share;  // next step, end of this CTA's run, run length S
@@ -48,16 +49,17 @@ struct Work {
   __device__ __forceinline__ void enter(const CacheAttnParams& p, int request) {
     r = request;
     q = request_at(p, r);
-    chunks = (q.rows + ROWS - 1) / ROWS;
+    chunks = (q.rows + unit_rows - 1) / unit_rows;
     steps = q.L > 0 ? (q.L + KEYS - 1) / KEYS : 1;
   }
-  static __device__ __forceinline__ int64_t steps_of(const CacheAttnParams& p, int r) {
+  __device__ __forceinline__ int64_t steps_of(const CacheAttnParams& p, int r) const {
     const Request q = request_at(p, r);
-    return (int64_t)((q.rows + ROWS - 1) / ROWS) * p.c.heads * (q.L > 0 ? (q.L + KEYS - 1) / KEYS : 1);
+    return (int64_t)((q.rows + unit_rows - 1) / unit_rows) * p.c.heads * (q.L > 0 ? (q.L + KEYS - 1) / KEYS : 1);
   }
   // The first unit of this CTA's run.  All threads of the block (a multiple of 32, at most 1024) call it.
   // min_share: runs are not made shorter than this.
-  __device__ __forceinline__ bool start(const CacheAttnParams& p, int64_t (&s_sum)[33], int64_t (&s_out)[3], int min_share) {
+  __device__ __forceinline__ bool start(const CacheAttnParams& p, int rows, int64_t (&s_sum)[33], int64_t (&s_out)[3], int min_share) {
+    unit_rows = rows;
     const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int per = (p.R + T - 1) / T, b0 = min(p.R, t * per), b1 = min(p.R, b0 + per);
     int64_t sum = 0;
@@ -125,6 +127,22 @@ struct Work {
   __device__ __forceinline__ int last_cta() const { return (int)((pos - step + steps - 1) / share); }
 };
 
+// pair i of a word of codes as bf16 (16 + low, 16 + high): the nibbles moved to the top mantissa bits under the
+// exponent of 16
+template <int I>
+__device__ __forceinline__ uint32_t pair16(uint32_t w) {
+  const uint32_t s = I == 0 ? w << 3 : I == 1 ? w >> 1 : I == 2 ? w >> 5 : w >> 9;
+  return (s & 0x00780078u) | 0x41804180u;
+}
+// such a pair as values, minimum + step * code, each rounded once
+__device__ __forceinline__ uint32_t value2(uint32_t c16, uint32_t step, uint32_t mn) {
+  uint32_t c, r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(c16), "r"(0x41804180u));  // exact
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(step), "r"(mn));
+  return r;
+}
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

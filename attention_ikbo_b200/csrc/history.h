@@ -78,6 +78,14 @@ struct CacheAttnParams {
 constexpr int kFewRows = 16;   // rows of a unit of the kernel for few rows
 size_t cache_few_part_bytes(int dh);
 int cache_few_grid(int sms);
+struct CacheManyParams {
+  CUtensorMap tm_q;          // Q viewed as [tokens][H][dh], box {64, G, 128 / G}
+  CacheAttnParams a;
+  int min_share;             // blocks of keys in a CTA's run, at least
+  long long wait_limit_ns;
+};
+size_t cache_many_part_bytes(int dh);  // partial results of one unit
+cudaError_t launch_cache_many(const CacheManyParams& p, int dh, int grid, cudaStream_t st);
 cudaError_t launch_cache_few(const CacheAttnParams& p, int dh, int grid, cudaStream_t st);
 
 }  // namespace rocs

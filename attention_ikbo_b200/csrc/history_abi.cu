@@ -8,6 +8,8 @@ namespace rocs {
 int sm_count_ext();
 int check_csr_ext(const int32_t* off, int64_t R, int64_t* total);
 void set_last_launches(int n);
+bool tmap_bf16_3d_ext(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer1, uint64_t outer2, uint64_t row_bytes,
+                      uint64_t plane_bytes, uint32_t box_in, uint32_t box_1, uint32_t box_2);
 }  // namespace rocs
 
 using namespace rocs;
@@ -171,15 +173,17 @@ int cache_move(const rocs_cache_move_args* a, bool append, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------- attention over the cache
+constexpr int kFewLimit = 32;   // rows of a key head up to which a request goes to the kernel for few rows
+constexpr int kMaxShared = 64;  // query heads to a key head up to which a 128-row tile is well filled
 inline size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
 
 // What a call needs: which kernels run (by the rows of a key head that the requests have), and the workspace
 // [WsHeader][counters][partial results], the first two zeroed before every call.
 struct AttnPlan {
   int64_t C = 0;
-  bool few = false;
-  int grid_few = 0;
-  size_t zero = 0, bytes = 0;
+  int rows_hi = 0;  // requests with up to this many rows go to the kernel for few rows
+  int grid_few = 0, grid_many = 0;  // 0: not launched
+  size_t cnt_many = 0, zero = 0, bytes = 0;
 };
 
 int attn_validate(const rocs_dca_cache_args* a, AttnPlan* pl) {
@@ -203,16 +207,19 @@ int attn_validate(const rocs_dca_cache_args* a, AttnPlan* pl) {
     const int64_t row = a->H * a->cache.dh;
     if (a->q_ld != 0 && a->q_ld < row) return ROCS_ERR_INVALID_ARG;
     if (a->q_ld % 8 || a->q_ld >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
-    pl->few = true;
+    const int64_t G = a->H / a->cache.heads;
+    pl->rows_hi = G > kMaxShared ? 0x7fffffff : kFewLimit;
+    for (int64_t r = 0; r < a->R && (!pl->grid_few || !pl->grid_many); ++r) {
+      const int64_t rows = (a->cand_off_host[r + 1] - a->cand_off_host[r]) * a->q * G;
+      if (rows > pl->rows_hi) pl->grid_many = sm_count_ext();
+      else if (rows > 0) pl->grid_few = cache_few_grid(sm_count_ext());
+    }
   }
-  pl->zero = sizeof(WsHeader);
-  size_t part = 0;
-  if (pl->few) {
-    pl->grid_few = cache_few_grid(sm_count_ext());
-    pl->zero += a256(sizeof(int) * (size_t)pl->grid_few);
-    part = 2 * (size_t)pl->grid_few * cache_few_part_bytes((int)a->cache.dh);
-  }
-  pl->bytes = pl->zero + part;
+  const size_t part_few = 2 * (size_t)pl->grid_few * cache_few_part_bytes((int)a->cache.dh);
+  const size_t part_many = 2 * (size_t)pl->grid_many * cache_many_part_bytes((int)a->cache.dh);
+  pl->cnt_many = sizeof(WsHeader) + a256(sizeof(int) * (size_t)pl->grid_few);
+  pl->zero = pl->cnt_many + a256(8 * sizeof(int) * (size_t)pl->grid_many);
+  pl->bytes = pl->zero + (part_few > part_many ? part_few : part_many);  // one kernel after the other
   return ROCS_OK;
 }
 
@@ -254,11 +261,26 @@ int rocs_dca_cache_forward(const rocs_dca_cache_args* a, rocs_stream_t stream) {
   p.ws = reinterpret_cast<WsHeader*>(ws);
   p.part = reinterpret_cast<float*>(ws + pl.zero);
   int launches = 0;
-  if (pl.few) {
+  if (pl.grid_few) {
     p.rows_lo = 0;
-    p.rows_hi = 0x7fffffff;
+    p.rows_hi = pl.rows_hi;
     p.cnt = reinterpret_cast<int*>(ws + sizeof(WsHeader));
     if (launch_cache_few(p, (int)a->cache.dh, pl.grid_few, st) != cudaSuccess) return ROCS_ERR_CUDA;
+    ++launches;
+  }
+  if (pl.grid_many) {
+    CacheManyParams m;
+    std::memset(&m, 0, sizeof(m));
+    if (!tmap_bf16_3d_ext(&m.tm_q, p.q, (uint64_t)a->cache.dh, (uint64_t)a->H, (uint64_t)(pl.C * a->q), (uint64_t)a->cache.dh * 2,
+                          (uint64_t)p.q_ld * 2, 64, (uint32_t)p.G, (uint32_t)(128 / p.G)))
+      return ROCS_ERR_CUDA;
+    m.a = p;
+    m.a.rows_lo = pl.rows_hi;
+    m.a.rows_hi = 0x7fffffff;
+    m.a.cnt = reinterpret_cast<int*>(ws + pl.cnt_many);
+    m.min_share = 2;
+    m.wait_limit_ns = kDefaultWaitLimitNs;
+    if (launch_cache_many(m, (int)a->cache.dh, pl.grid_many, st) != cudaSuccess) return ROCS_ERR_CUDA;
     ++launches;
   }
   set_last_launches(launches);

@@ -90,12 +90,12 @@ bool tmap_bf16(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer
 
 // 3-D view [outer2][outer1][inner] with rows of row_bytes and planes of plane_bytes
 bool tmap_bf16_3d(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer1, uint64_t outer2,
-                  uint64_t row_bytes, uint64_t plane_bytes, uint32_t box_in, uint32_t box_1) {
+                  uint64_t row_bytes, uint64_t plane_bytes, uint32_t box_in, uint32_t box_1, uint32_t box_2 = 1) {
   EncodeTiledFn f = encode_fn();
   if (!f || !base || inner == 0 || outer1 == 0 || outer2 == 0) return false;
   cuuint64_t dims[3] = {inner, outer1, outer2};
   cuuint64_t strides[2] = {row_bytes, plane_bytes};
-  cuuint32_t box[3] = {box_in, box_1, 1};
+  cuuint32_t box[3] = {box_in, box_1, box_2};
   cuuint32_t es[3] = {1, 1, 1};
   return f(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -418,6 +418,10 @@ size_t dca_body_bytes_ext(int64_t R, int64_t n_units) { return dca_body(R, n_uni
 int64_t dca_units_ext(const rocs_dca_args* a) { return dca_units(a); }
 void set_last_launches(int n) { g_last_launches = n; }
 int sm_count_ext() { return sm_count(); }
+bool tmap_bf16_3d_ext(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer1, uint64_t outer2, uint64_t row_bytes,
+                      uint64_t plane_bytes, uint32_t box_in, uint32_t box_1, uint32_t box_2) {
+  return tmap_bf16_3d(tm, base, inner, outer1, outer2, row_bytes, plane_bytes, box_in, box_1, box_2);
+}
 int check_csr_ext(const int32_t* off, int64_t R, int64_t* total) { return check_csr(off, R, total); }
 std::atomic<uint64_t>& configured_device_mask_ref() {
   static std::atomic<uint64_t> mask{0};
