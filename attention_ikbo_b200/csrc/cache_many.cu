@@ -10,11 +10,11 @@
 //     two packed FMAs for two scores where a plain softmax has one: scores are exact up to fp32 sums.  Rounding the
 //     keys to bf16 instead would put 2^-9 of every product into the scores.
 //   * V is rounded to bf16 once, as P is and as the output is: its error is a weighted mean of such roundings.
-// Warp roles (512 threads): warp 0 loads query tiles by TMA, warp 1 issues tcgen05.mma, warps 4-7 and 8-11 are the
+// Warp roles (512 threads): warp 0 loads query tiles by TMA, warp 1 issues tcgen05.mma, warp 2 walks the work and copies
+// codes, steps and minima into staging buffers (cp.async.bulk, one copy for each page), warps 4-7 and 8-11 are the
 // softmax and the epilogue of query tiles A and B (S in TMEM; P in bf16 over S, the A operand of P V; O in TMEM), warps
-// 12-15 turn codes into the tensor core's 128-byte-swizzled operand tiles: codes go from global memory into registers
-// one block ahead, through the logic operations, into a ring of shared-memory slots in the order of their use.
-// setmaxnreg moves registers to the softmax warps, which hold a row's 128 scores.
+// 12-15 turn staged codes into the tensor core's 128-byte-swizzled operand tiles, into a ring of slots in the order of
+// their use.  setmaxnreg moves registers to the softmax warps.
 // Work is shared out by cache_work.cuh: equal runs of blocks, partial results merged by the last to finish.
 //
 // The rows of a tile are whole query tokens of the G heads that share the key head: row = token * G + head, 128 / G
@@ -27,25 +27,42 @@ namespace {
 
 constexpr int kThreadsMany = 512, BM = 128, BN = 128;
 constexpr int kSoftWarp = 4, kDeqWarp = 12;
-constexpr int kSlots = 8;  // of the scale ring and the per-unit records: far more than the K/V ring lets run ahead
+constexpr int kRecs = 4;  // records of units on their way through the roles
 // 4 warpgroups launched at 128 registers a thread; the shares add up to what was launched
-constexpr uint32_t kLaunchRegs = 128, kRegsCtl = 56, kRegsDeq = 88, kRegsSoft = 184;
+constexpr uint32_t kLaunchRegs = 128, kRegsCtl = 64, kRegsDeq = 80, kRegsSoft = 184;
 static_assert(kRegsCtl + kRegsDeq + 2 * kRegsSoft == 4 * kLaunchRegs, "register split");
+
+// One unit's run of key blocks, as warp 2 hands it to the other roles.
+struct Rec {
+  int c0, rows, L, head;  // first candidate, query rows of the key head, keys of the history, key head
+  int row0, step, n;      // first row of tile A, first block of 128 keys, blocks (-1: no more units)
+  int cta0, cta1;         // CTAs whose runs hold blocks of the unit
+  int bad;                // first key whose V is not finite
+  int pad[6];
+};
 
 template <int DH>
 struct ManySmem {
   static constexpr uint32_t kTile = BM * DH * 2;  // a query tile, or one block of K or V (bf16)
   static constexpr int kRing = DH == 128 ? 4 : 6;
-  static constexpr uint32_t kStage = 32 * 64;     // per softmax warp: 32 rows x 32 columns of O (bf16)
+  static constexpr int kStaged = DH == 128 ? 2 : 4;
+  static constexpr uint32_t kStaging = BN * DH / 2 + BN * 4;  // codes, then steps and minima
+  // Steps and minima of a K block stay until both tiles' softmax is done with it.  A block is converted once the ring
+  // slot kRing items before it is free.  At dh = 128 that item is at the earliest the K block before the last, whose S
+  // was issued after P of the block before it: four slots are enough.  At dh = 64 S runs ahead of P: eight.
+  static constexpr int kScales = DH == 128 ? 4 : 8;
+  static constexpr uint32_t kOut = 32 * 32;       // per softmax warp: 32 rows x 16 columns of O (bf16)
   static constexpr uint32_t off_q = 0;
   static constexpr uint32_t off_ring = 2 * kTile;
-  static constexpr uint32_t off_stage = off_ring + kRing * kTile;
-  static constexpr uint32_t off_scale = off_stage + 8 * kStage;  // kSlots x 64 key pairs x {a0, a1, b0, b1}
-  static constexpr uint32_t off_bar = off_scale + kSlots * BN * 8;
-  static constexpr uint32_t n_bars = 2 * kRing + 2 * 8 + 1 + 2 * kSlots;
+  static constexpr uint32_t off_staging = off_ring + kRing * kTile;
+  static constexpr uint32_t off_out = off_staging + kStaged * kStaging;
+  static constexpr uint32_t off_scale = off_out + 8 * kOut;  // kScales x 64 key pairs x {a0, a1, b0, b1}
+  static constexpr uint32_t off_rec = off_scale + kScales * BN * 8;
+  static constexpr uint32_t off_bar = off_rec + kRecs * sizeof(Rec);
+  static constexpr uint32_t n_bars = 2 * kRing + 2 * 8 + 1 + kScales + 3 * kRecs + 2 * kStaged;
   static constexpr uint32_t off_misc = off_bar + n_bars * 8;
-  static constexpr uint32_t alloc_bytes = off_misc + 64 + 1024;
-  static_assert(alloc_bytes <= 232448 - 1024, "shared memory budget");
+  static constexpr uint32_t alloc_bytes = off_misc + 16 + 1024;
+  static_assert(alloc_bytes <= 232448 - 512, "shared memory budget");
 };
 template <int DH>
 constexpr int many_slab() { return 32 * (DH + 2); }  // floats of a partial result of 32 rows: O [dh/4][32][4], m, l
@@ -60,6 +77,15 @@ __device__ __forceinline__ void wait_ld_regs(uint32_t (&a)[32], uint32_t (&b)[32
                  "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15]),
                  "+r"(b[16]), "+r"(b[17]), "+r"(b[18]), "+r"(b[19]), "+r"(b[20]), "+r"(b[21]), "+r"(b[22]), "+r"(b[23]),
                  "+r"(b[24]), "+r"(b[25]), "+r"(b[26]), "+r"(b[27]), "+r"(b[28]), "+r"(b[29]), "+r"(b[30]), "+r"(b[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void wait_ld_regs32(uint32_t (&a)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
+                 "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]),
+                 "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31])
                :
                : "memory");
 }
@@ -88,13 +114,11 @@ __device__ __forceinline__ void ld_shared_2x64(uint32_t addr, uint64_t& a, uint6
   asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
 
-// One block of K or V on its way into a ring slot.
-struct Item {
-  int page0, page1;  // pages of this warp's two 16-key granules
-  int key0, left;    // first key, keys of the history from there on
-  int head;
-  int flags;         // bit 0: V, 1: last block of the unit's run, 2: there is an item; from bit 4: unit
-};
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
 
 }  // namespace
 
@@ -119,11 +143,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
   uint64_t* s_free = o_empty + 2;    // [2] separate P: S read into registers
   uint64_t* pv_done = s_free + 2;    // [2] separate P: P V complete (P may be rewritten)
   uint64_t* drain_bar = pv_done + 2;
-  uint64_t* sc_full = drain_bar + 1;      // [kSlots] steps and minima of a K block are there
-  uint64_t* unit_done = sc_full + kSlots;  // [kSlots] all V blocks of a unit have been looked through
+  uint64_t* sc_full = drain_bar + 1;           // [kScales] steps and minima of a K block are there
+  uint64_t* rec_full = sc_full + L::kScales;   // [kRecs]
+  uint64_t* rec_empty = rec_full + kRecs;      // [kRecs] read by every role, and the unit's epilogues done
+  uint64_t* rec_v = rec_empty + kRecs;         // [kRecs] all V blocks of the unit have been looked through
+  uint64_t* st_full = rec_v + kRecs;           // [kStaged]
+  uint64_t* st_empty = st_full + L::kStaged;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + L::off_misc);
   int* s_abort = reinterpret_cast<int*>(smem + L::off_misc + 4);
-  int* s_bad = reinterpret_cast<int*>(smem + L::off_misc + 16);  // [kSlots] first key of the unit whose V is not finite
+  volatile Rec* recs = reinterpret_cast<volatile Rec*>(smem + L::off_rec);
   __shared__ int64_t s_sum[33], s_out[3];
 
   const int warp = threadIdx.x >> 5;
@@ -149,10 +177,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
       mbar_init(&pv_done[x], 1);
     }
     mbar_init(drain_bar, 1);
-    for (int k = 0; k < kSlots; ++k) {
-      mbar_init(&sc_full[k], 4);
-      mbar_init(&unit_done[k], 4);
-      s_bad[k] = 0x7fffffff;
+    for (int k = 0; k < L::kScales; ++k) mbar_init(&sc_full[k], 4);
+    for (int k = 0; k < kRecs; ++k) {
+      mbar_init(&rec_full[k], 1);
+      mbar_init(&rec_empty[k], 1 + 1 + 4 + 8);  // query tiles, issuer, conversion warps, softmax warps
+      mbar_init(&rec_v[k], 4);
+    }
+    for (int k = 0; k < L::kStaged; ++k) {
+      mbar_init(&st_full[k], 1);
+      mbar_init(&st_empty[k], 4);
     }
     *s_abort = 0;
     fence_mbar_init();
@@ -174,6 +207,17 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
   constexpr bool kSepP = 256 + 2 * DH + 128 <= 512;
   constexpr uint32_t kPCol = 256 + 2 * DH;
 
+  int ri = 0;
+  uint32_t rec_ph = 0;  // this role's place among the unit records
+  // the next unit's record; null after the last one, or when a wait has run out
+  auto next_rec = [&](int where) -> volatile Rec* {
+    if (!mbar_wait(&rec_full[ri], rec_ph, ctl, where)) return nullptr;
+    return recs[ri].n < 0 ? nullptr : &recs[ri];
+  };
+  auto rec_step = [&]() {
+    if (++ri == kRecs) { ri = 0; rec_ph ^= 1; }
+  };
+
   if (warp < kSoftWarp) {
     reg_dealloc<kRegsCtl>();
     if (warp == 0 && lane == 0) {
@@ -181,29 +225,103 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
       tma_prefetch_desc(&mp.tm_q);
       uint32_t ph[2] = {0, 0}, n[2] = {0, 0};
       bool ok = true;
-      for (bool more = true; more && ok; more = w.next(p)) {
-        if (w.q.L == 0) continue;
-        const int row0 = w.chunk * 2 * tile_rows, nx = row0 + tile_rows < w.q.rows ? 2 : 1;
-        const int tok0 = w.q.c0 * p.q_tokens + w.chunk * 2 * tile_tokens;
-        for (int x = 0; x < nx; ++x) {
-          if (!mbar_wait(&q_empty[x], ph[x] ^ 1, ctl, 941)) { ok = false; break; }
+      while (volatile Rec* r = next_rec(940)) {
+        const int keys = r->L, nx = r->row0 + tile_rows < r->rows ? 2 : 1, head = r->head;
+        const int tok0 = r->c0 * p.q_tokens + r->row0 / p.G;
+        mbar_arrive(&rec_empty[ri]);
+        rec_step();
+        if (keys == 0) continue;
+        for (int x = 0; x < nx && ok; ++x) {
+          if (!(ok = mbar_wait(&q_empty[x], ph[x] ^ 1, ctl, 941))) break;
           ph[x] ^= 1;
           ++n[x];
           mbar_arrive_expect_tx(&q_full[x], (uint32_t)tile_rows * DH * 2);
 #pragma unroll
           for (int cc = 0; cc < DH / 64; ++cc)
-            tma_load_3d(s_q + x * L::kTile + cc * (BM * 128), &mp.tm_q, &q_full[x], cc * 64, w.head * p.G, tok0 + x * tile_tokens);
+            tma_load_3d(s_q + x * L::kTile + cc * (BM * 128), &mp.tm_q, &q_full[x], cc * 64, head * p.G, tok0 + x * tile_tokens);
         }
+        if (!ok) break;
       }
-      if (!ok)
+      if (ctl.aborted())
         for (int x = 0; x < 2; ++x)
           if (n[x]) mbar_drain(&q_full[x], (n[x] - 1) & 1, 20000000ull);
+    } else if (warp == 2) {
+      // ------------------------------------------------------------------ work, codes
+      int si = 0, n_issued = 0;
+      uint32_t sph = 0;
+      const int page = 1 << p.c.page_log2;
+      const bool mine = lane < 8 && (lane * 16 & (page - 1)) == 0;  // a page starts at this lane's 16 keys of the block
+      const uint32_t code_bytes = page * (DH / 2), scale_bytes = page * 4;
+      const uint32_t staging = smem_u32(smem + L::off_staging);
+      bool ok = true;
+      for (bool more = true; more && ok; more = w.next(p)) {
+        if (!(ok = mbar_wait(&rec_empty[ri], rec_ph ^ 1, ctl, 952))) break;
+        const int n = w.count(), keys = w.q.L;
+        if (lane == 0) {
+          volatile Rec& r = recs[ri];
+          r.c0 = w.q.c0;
+          r.rows = w.q.rows;
+          r.L = keys;
+          r.head = w.head;
+          r.row0 = w.chunk * 2 * tile_rows;
+          r.step = w.step;
+          r.n = n;
+          r.cta0 = w.first_cta();
+          r.cta1 = w.last_cta();
+          r.bad = 0x7fffffff;
+          mbar_arrive(&rec_full[ri]);
+        }
+        rec_step();
+        if (keys == 0) continue;
+        const int32_t* table = p.table + (int64_t)w.r * p.max_pages;
+        auto page_at = [&](int j) {
+          const int key = (w.step + j) * BN + (int)lane * 16;
+          return j < n && mine && key < keys ? table[key >> p.c.page_log2] : 0;
+        };
+        auto copy = [&](int kv, int j, int pg) -> bool {
+          if (!mbar_wait(&st_empty[si], sph ^ 1, ctl, 953)) return false;
+          const int key = (w.step + j) * BN + (int)lane * 16;
+          const bool go = mine && key < keys;
+          if (go && (unsigned)pg >= (unsigned)p.c.pages) {
+            record_error(p.ws, ROCS_ERR_DEVICE_INDEX, 951);
+            pg = 0;
+          }
+          const uint32_t count = __popc(__ballot_sync(0xffffffffu, go));
+          if (lane == 0) mbar_arrive_expect_tx(&st_full[si], count * (code_bytes + scale_bytes));
+          __syncwarp();
+          if (go) {
+            const int64_t row = ((int64_t)pg * p.c.heads + w.head) << p.c.page_log2;
+            const uint32_t dst = staging + si * L::kStaging;
+            bulk_load(dst + lane * 16 * (DH / 2), p.c.codes[kv] + row * (DH / 2), code_bytes, &st_full[si]);
+            bulk_load(dst + BN * (DH / 2) + lane * 64, p.c.scale[kv] + row, scale_bytes, &st_full[si]);
+          }
+          ++n_issued;
+          if (++si == L::kStaged) { si = 0; sph ^= 1; }
+          return true;
+        };
+        // blocks in the order of their use: K0, K1, V0, K2, V1, ..., V_last
+        int now = 0, next = page_at(0);
+        for (int j = 0; j < n && ok; ++j) {
+          const int before = now;
+          now = next;
+          next = page_at(j + 1);
+          ok = copy(0, j, now) && (j == 0 || copy(1, j - 1, before));
+        }
+        if (ok) ok = copy(1, n - 1, now);
+      }
+      if (ok && mbar_wait(&rec_empty[ri], rec_ph ^ 1, ctl, 954) && lane == 0) {
+        recs[ri].n = -1;
+        mbar_arrive(&rec_full[ri]);
+      }
+      if (ctl.aborted())
+        for (int k = n_issued > L::kStaged ? n_issued - L::kStaged : 0; k < n_issued; ++k)
+          mbar_drain(&st_full[k % L::kStaged], (k / L::kStaged) & 1, 20000000ull);
     } else if (warp == 1 && lane == 0) {
       // ------------------------------------------------------------------ tcgen05 issuer
       constexpr uint32_t idesc_s = idesc_bf16(BM, BN, false, false);  // S = Q (16 + c)^T: both K-major
       constexpr uint32_t idesc_o = idesc_bf16(BM, DH, false, true);   // O += P V: V is MN-major
       uint32_t rs = 0, rph = 0, qph = 0, pph = 0, oeph = 0, sfph = 0;  // phase bits of the two tiles
-      bool s_pend[2] = {false, false}, b_pend = false;
+      bool s_pend[2] = {false, false};
       bool ok = true;
       const uint32_t q0 = smem_u32(s_q), ring0 = smem_u32(s_ring);
       uint32_t slot = 0;
@@ -247,9 +365,11 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         if (kSepP) umma_commit(&pv_done[x]);
         return true;
       };
-      for (bool more = true; more; more = w.next(p)) {
-        if (w.q.L == 0) continue;
-        const int nx = w.chunk * 2 * tile_rows + tile_rows < w.q.rows ? 2 : 1, n = w.count();
+      while (volatile Rec* r = next_rec(955)) {
+        const int keys = r->L, nx = r->row0 + tile_rows < r->rows ? 2 : 1, n = r->n;
+        mbar_arrive(&rec_empty[ri]);
+        rec_step();
+        if (keys == 0) continue;
         for (int x = 0; x < nx && ok; ++x) {
           ok = mbar_wait(&q_full[x], (qph >> x) & 1, ctl, 945);
           qph ^= 1u << x;
@@ -258,11 +378,6 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         for (int x = 0; x < nx && ok; ++x) ok = issue_s(x);
         if (!ok) break;
         umma_commit(&ring_empty[slot]);
-        // a unit without tile B still waits for the end of B's last unit, so that no record of an older unit is reused
-        if (nx == 2) b_pend = true;
-        else if (b_pend) {
-          if (!(ok = mbar_wait(&o_empty[1], ((oeph >> 1) & 1) ^ 1, ctl, 947))) break;
-        }
         for (int j = 1; j < n && ok; ++j) {
           if (!(ok = take(948))) break;
           const uint32_t kslot = slot;
@@ -306,132 +421,87 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
     constexpr int RPI = 32 / PARTS;    // rows of one load instruction
     constexpr int ITER = 32 / RPI;     // loads for this warp's 32 keys
     const int dw = warp - kDeqWarp, part = lane % PARTS, sub = lane / PARTS;
-    const int page_mask = (1 << p.c.page_log2) - 1;
+    const uint32_t staging = smem_u32(smem + L::off_staging), scales = smem_u32(smem + L::off_scale), ring = smem_u32(s_ring);
     const float cl = p.scale_log2;
-    // blocks in the order of their use: K0, K1, V0, K2, V1, ..., V_last of every unit
-    bool more = true;
-    int n = 0, i = 0, unit = -1;
-    auto unit_start = [&]() {
-      while (more && w.q.L == 0) more = w.next(p);
-      if (more) {
-        n = w.count();
-        i = 0;
-        ++unit;
-      }
-    };
-    unit_start();
-    auto gen = [&](Item& it) {
-      it.flags = 0;
-      it.left = 0;
-      if (!more) return;
-      const int v = i > 0 && ((i & 1) == 0 || i == 2 * n - 1);
-      const int j = i == 2 * n - 1 ? n - 1 : v ? i / 2 - 1 : (i + 1) / 2;
-      it.key0 = (w.step + j) * BN;
-      it.left = w.q.L - it.key0;
-      it.head = w.head;
-      it.flags = v | (i == 2 * n - 1 ? 2 : 0) | 4 | (unit << 4);
-      const int32_t* t = p.table + (int64_t)w.r * p.max_pages;
-      const int k0 = it.key0 + 32 * dw;
-      it.page0 = 32 * dw < it.left ? t[k0 >> p.c.page_log2] : 0;
-      it.page1 = 32 * dw + 16 < it.left ? t[(k0 + 16) >> p.c.page_log2] : 0;
-      if (++i == 2 * n) {
-        more = w.next(p);
-        unit_start();
-      }
-    };
-    auto load = [&](Item& it, uint4 (&c)[ITER], uint32_t& sc) {
-      if (!(it.flags & 4)) return;
-      if ((unsigned)it.page0 >= (unsigned)p.c.pages || (unsigned)it.page1 >= (unsigned)p.c.pages) {
-        if (lane == 0) record_error(p.ws, ROCS_ERR_DEVICE_INDEX, 951);
-        if ((unsigned)it.page0 >= (unsigned)p.c.pages) it.page0 = 0;
-        if ((unsigned)it.page1 >= (unsigned)p.c.pages) it.page1 = 0;
-      }
-      const int kv = it.flags & 1, k0 = it.key0 + 32 * dw;
-      const int64_t row0 = (((int64_t)it.page0 * p.c.heads + it.head) << p.c.page_log2) + (k0 & page_mask);
-      const int64_t row1 = (((int64_t)it.page1 * p.c.heads + it.head) << p.c.page_log2) + ((k0 + 16) & page_mask) - 16;
-#pragma unroll
-      for (int s = 0; s < ITER; ++s) {
-        const int key = RPI * s + sub;
-        c[s] = make_uint4(0, 0, 0, 0);
-        if (32 * dw + key < it.left)
-          c[s] = *reinterpret_cast<const uint4*>(p.c.codes[kv] + ((key < 16 ? row0 : row1) + key) * (DH / 2) + part * 16);
-      }
-      sc = 0;
-      if (32 * dw + (int)lane < it.left)
-        sc = *reinterpret_cast<const uint32_t*>(p.c.scale[kv] + ((int)lane < 16 ? row0 : row1) + lane);
-    };
-    uint32_t rs = 0, rph = 0, kord = 0;
-    auto convert = [&](const Item& it, const uint4 (&c)[ITER], uint32_t sc) -> bool {
-      if (!mbar_wait(&ring_empty[rs], rph ^ 1, ctl, 952)) return false;
-      const uint32_t slot = smem_u32(s_ring) + rs * L::kTile;
-      float st = __uint_as_float(sc << 16), mn = __uint_as_float(sc & 0xffff0000u);
-      const int u = (it.flags >> 4) & (kSlots - 1);
-      if (!(it.flags & 1)) {
-        // a and b of this lane's key, in pairs {a0, a1, b0, b1}
-        const uint32_t at = smem_u32(smem + L::off_scale) + (kord & (kSlots - 1)) * (BN * 8) + (16 * dw + (lane >> 1)) * 16 + (lane & 1) * 4;
-        const float a = cl * st, b = fmaf(-16.0f, a, cl * mn);
-        st_shared_u32(at, __float_as_uint(a));
-        st_shared_u32(at + 8, __float_as_uint(b));
-      } else {
-        // a row with values that are not finite: zeros here, and NaN for the rows that see it (in the epilogue)
-        const bool bad = !(fabsf(mn) + 15.0f * fabsf(st) <= 3.38e38f);
-        const unsigned any = __ballot_sync(0xffffffffu, bad);
-        if (any) {
-          if (lane == 0) atomicMin(&s_bad[u], it.key0 + 32 * dw + __ffs(any) - 1);
-          if (bad) sc = 0;
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < ITER; ++s) {
-        const int key = RPI * s + sub, row = 32 * dw + key;
-        const uint32_t base = slot + (part >> 1) * (BN * 128) + row * 128;
-        const uint32_t x4 = (part & 1) * 4, sw = row & 7;
-        const uint32_t cw[4] = {c[s].x, c[s].y, c[s].z, c[s].w};
-        if (!(it.flags & 1)) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            st_shared_v4(base + (((x4 + k) ^ sw) << 4), pair16<0>(cw[k]), pair16<1>(cw[k]), pair16<2>(cw[k]), pair16<3>(cw[k]));
-        } else {
-          const uint32_t rsc = __shfl_sync(0xffffffffu, sc, key);
-          const uint32_t st2 = __byte_perm(rsc, rsc, 0x1010), mn2 = __byte_perm(rsc, rsc, 0x3232);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            st_shared_v4(base + (((x4 + k) ^ sw) << 4), value2(pair16<0>(cw[k]), st2, mn2), value2(pair16<1>(cw[k]), st2, mn2),
-                         value2(pair16<2>(cw[k]), st2, mn2), value2(pair16<3>(cw[k]), st2, mn2));
-        }
-      }
-      fence_proxy_async_smem();
+    uint32_t rs = 0, rph = 0, si = 0, sph = 0, kord = 0;
+    bool ok = true;
+    while (ok) {
+      volatile Rec* r = next_rec(956);
+      if (!r) break;
+      const int step = r->step, n = r->n, keys = r->L, rec = ri;
       __syncwarp();
-      if (lane == 0) {
-        if (!(it.flags & 1)) mbar_arrive(&sc_full[kord & (kSlots - 1)]);
-        if (it.flags & 2) {
-          // the record of a unit four further on: its last reader is long done, its first writer not there yet
-          if (dw == 0) s_bad[(u + 4) & (kSlots - 1)] = 0x7fffffff;
-          mbar_arrive(&unit_done[u]);
-        }
-        mbar_arrive(&ring_full[rs]);
-      }
-      if (!(it.flags & 1)) ++kord;
-      if (++rs == kRing) { rs = 0; rph ^= 1; }
-      return true;
-    };
-    Item it0, it1, it2;
-    uint4 c0[ITER], c1[ITER];
-    uint32_t sc0 = 0, sc1 = 0;
-    gen(it0);
-    load(it0, c0, sc0);
-    gen(it1);
-    load(it1, c1, sc1);
-    gen(it2);
-    while (it0.flags & 4) {
-      if (!convert(it0, c0, sc0)) break;
-      it0 = it1;
+      if (lane == 0) mbar_arrive(&rec_empty[ri]);
+      rec_step();
+      if (keys == 0) continue;
+      for (int i = 0; i < 2 * n; ++i) {
+        const bool v = i > 0 && ((i & 1) == 0 || i == 2 * n - 1);
+        const int j = i == 2 * n - 1 ? n - 1 : v ? i / 2 - 1 : (i + 1) / 2;
+        const int key0 = (step + j) * BN + 32 * dw, left = keys - key0;  // this warp's 32 keys, and how many there are
+        if (!(ok = mbar_wait(&st_full[si], sph, ctl, 957))) break;
+        const uint32_t src = staging + si * L::kStaging;
+        uint32_t sc;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc) : "r"(src + BN * (DH / 2) + (32 * dw + lane) * 4) : "memory");
+        uint4 c[ITER];
 #pragma unroll
-      for (int s = 0; s < ITER; ++s) c0[s] = c1[s];
-      sc0 = sc1;
-      it1 = it2;
-      load(it1, c1, sc1);
-      gen(it2);
+        for (int s = 0; s < ITER; ++s) c[s] = ld_shared_v4(src + (32 * dw + RPI * s + sub) * (DH / 2) + part * 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st_empty[si]);
+        if ((int)lane >= left) sc = 0;  // places past the history: codes are always finite, a zero step makes zeros of V
+        if (!(ok = mbar_wait(&ring_empty[rs], rph ^ 1, ctl, 958))) break;
+        const uint32_t slot = ring + rs * L::kTile + (part >> 1) * (BN * 128);
+        // Bank conflicts: 8 lanes of a store are two rows times four parts; parts 2 and 3 are in another chunk of 64
+        // channels at the same banks, and take their words in another order
+        const uint32_t swap = (part >> 1) << 1;
+        if (!v) {
+          // a and b of this lane's key, in pairs {a0, a1, b0, b1}
+          const uint32_t at = scales + (kord % L::kScales) * (BN * 8) + (16 * dw + (lane >> 1)) * 16 + (lane & 1) * 4;
+          const float a = cl * bf_lo(sc), b = fmaf(-16.0f, a, cl * bf_hi(sc));
+          st_shared_u32(at, __float_as_uint(a));
+          st_shared_u32(at + 8, __float_as_uint(b));
+#pragma unroll
+          for (int s = 0; s < ITER; ++s) {
+            const int row = 32 * dw + RPI * s + sub;
+            const uint32_t cw[4] = {c[s].x, c[s].y, c[s].z, c[s].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t x = swap ? cw[k ^ 2] : cw[k];
+              st_shared_v4(slot + row * 128 + (((((part & 1) << 2) | (k ^ swap)) ^ (row & 7)) << 4), pair16<0>(x), pair16<1>(x),
+                           pair16<2>(x), pair16<3>(x));
+            }
+          }
+        } else {
+          // a row with values that are not finite: zeros here, and NaN for the rows that see it (in the epilogue)
+          const bool bad = !(fabsf(bf_hi(sc)) + 15.0f * fabsf(bf_lo(sc)) <= 3.38e38f);
+          const unsigned any = __ballot_sync(0xffffffffu, bad);
+          if (any) {
+            if (lane == 0) atomicMin(const_cast<int*>(&recs[rec].bad), key0 + __ffs(any) - 1);
+            if (bad) sc = 0;
+          }
+#pragma unroll
+          for (int s = 0; s < ITER; ++s) {
+            const int row = 32 * dw + RPI * s + sub;
+            const uint32_t cw[4] = {c[s].x, c[s].y, c[s].z, c[s].w};
+            const uint32_t rsc = __shfl_sync(0xffffffffu, sc, RPI * s + sub);
+            const uint32_t st2 = __byte_perm(rsc, rsc, 0x1010), mn2 = __byte_perm(rsc, rsc, 0x3232);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t x = swap ? cw[k ^ 2] : cw[k];
+              st_shared_v4(slot + row * 128 + (((((part & 1) << 2) | (k ^ swap)) ^ (row & 7)) << 4), value2(pair16<0>(x), st2, mn2),
+                           value2(pair16<1>(x), st2, mn2), value2(pair16<2>(x), st2, mn2), value2(pair16<3>(x), st2, mn2));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (!v) mbar_arrive(&sc_full[kord % L::kScales]);
+          if (i == 2 * n - 1) mbar_arrive(&rec_v[rec]);
+          mbar_arrive(&ring_full[rs]);
+        }
+        if (!v) ++kord;
+        if (++rs == kRing) { rs = 0; rph ^= 1; }
+        if (++si == L::kStaged) { si = 0; sph ^= 1; }
+      }
     }
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
@@ -442,35 +512,40 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
     const uint32_t s_addr = tmem_base + t_lane + x * 128;
     const uint32_t p_addr = kSepP ? tmem_base + t_lane + kPCol + x * 64 : s_addr;
     const uint32_t o_addr = tmem_base + t_lane + 256 + x * DH;
-    const uint32_t stage = smem_u32(smem + L::off_stage) + (warp - kSoftWarp) * L::kStage;
+    const uint32_t stage = smem_u32(smem + L::off_out) + (warp - kSoftWarp) * L::kOut;
     const uint32_t scales = smem_u32(smem + L::off_scale);
     const int trow = 32 * quarter + (int)lane;
     const uint32_t qrow = smem_u32(s_q) + x * L::kTile + trow * 128;
-    uint32_t kord = 0, unit = 0, qph = 0, sph = 0, oph = 0, n_sig = 0;
+    uint32_t kord = 0, qph = 0, sph = 0, oph = 0, n_sig = 0;
     bool ok = true;
-    for (bool more = true; more; more = w.next(p)) {
-      const Request& q = w.q;
-      const int row0 = (w.chunk * 2 + x) * tile_rows, n = w.count();
-      const bool row_ok = trow < tile_rows && row0 + trow < q.rows;
+    while (ok) {
+      volatile Rec* const r = next_rec(960);
+      if (!r) break;
+      const int rec = ri, v_ph = rec_ph, n = r->n, step = r->step;
+      const int row0 = r->row0 + x * tile_rows;
+      rec_step();
       // index of the row's (token, head) in the outputs, -1 for padding
-      int at = -1, lim = q.L;
-      if (row_ok) {
+      int at = -1, lim = r->L;
+      const bool empty = lim == 0;
+      if (trow < tile_rows && row0 + trow < r->rows) {
         const int tok = (row0 + trow) / p.G;
-        at = (q.c0 * p.q_tokens + tok) * p.H + w.head * p.G + (row0 + trow - tok * p.G);
-        if (p.key_limit) lim = min(lim, max(0, p.key_limit[q.c0 + tok / p.q_tokens]));
+        at = (r->c0 * p.q_tokens + tok) * p.H + r->head * p.G + (row0 + trow - tok * p.G);
+        if (p.key_limit) lim = min(lim, max(0, p.key_limit[r->c0 + tok / p.q_tokens]));
       }
-      if (q.L == 0) {
-        if (row_ok) {
+      if (empty) {
+        if (at >= 0) {
 #pragma unroll
           for (int k = 0; k < DH / 8; ++k) st_global_v4(p.o + (size_t)at * DH + 8 * k, 0u, 0u, 0u, 0u);
           if (p.lse) p.lse[at] = -INFINITY;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rec_empty[rec]);
         continue;
       }
-      const int u = unit & (kSlots - 1), uph = (unit / kSlots) & 1;
-      ++unit;
-      if (x == 1 && row0 >= q.rows) {
+      if (x == 1 && row0 >= r->rows) {
         kord += n;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rec_empty[rec]);
         continue;
       }
       const int lim_min = __reduce_min_sync(0xffffffffu, lim);
@@ -491,55 +566,77 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
 
       float m_used = -INFINITY, l = 0.0f;
       for (int j = 0; j < n; ++j, ++kord) {
-        const uint32_t sc = scales + (kord & (kSlots - 1)) * (BN * 8);
-        if (!(ok = mbar_wait(&sc_full[kord & (kSlots - 1)], (kord / kSlots) & 1, ctl, 962))) break;
+        const uint32_t sc = scales + (kord % L::kScales) * (BN * 8);
+        if (!(ok = mbar_wait(&sc_full[kord % L::kScales], (kord / L::kScales) & 1, ctl, 962))) break;
         if (!(ok = mbar_wait(&s_full[x], sph, ctl, 963))) break;
         sph ^= 1;
         tc_fence_after();
-        const int key0 = (w.step + j) * BN;
-        const bool careful = j == 0 || key0 + BN > lim_min;  // a first block, or one that some row does not see all of
-        uint32_t sv[4][32];
-        // first half of S, then the second half in flight while the first half's exponentials run
-        const bool split_ld = !kSepP && !careful;
-        tmem_ld32(s_addr, sv[0]);
-        tmem_ld32(s_addr + 32, sv[1]);
-        tmem_ld_wait();
-        tmem_ld32(s_addr + 64, sv[2]);
-        tmem_ld32(s_addr + 96, sv[3]);
-        if (!split_ld) wait_ld_regs(sv[2], sv[3]);
+        const int left = lim - (step + j) * BN;  // keys of the block that the row sees
+        const bool careful = j == 0 || (step + j + 1) * BN > lim_min;  // a first block, or one that some row does not see all of
+        // Scores in quarters of 32.  With P over S (dh = 128) P of quarter c lies over quarter c / 2, so quarters in
+        // order never overwrite an unread one; the first two stay in registers for the case that the block is done
+        // again, the last two can be read again.  With P apart all of S is read at once, and the next S may come.
+        constexpr int kBuf = kSepP ? 4 : 3;
+        uint32_t sv[kBuf][32];
+        auto buf = [](int c4) { return c4 < kBuf ? c4 : kBuf - 1; };
         if constexpr (kSepP) {
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(s_addr + c4 * 32, sv[c4]);
+          wait_ld_regs(sv[0], sv[1]);
+          wait_ld_regs(sv[2], sv[3]);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_free[x]);
-          if (n_sig > 0) {
+          if (n_sig > 0) {  // P is rewritten, and O rescaled, only after the last P V
             if (!(ok = mbar_wait(&pv_done[x], (n_sig - 1) & 1, ctl, 964))) break;
             tc_fence_after();
           }
+        } else {
+          tmem_ld32(s_addr, sv[0]);
+          tmem_ld32(s_addr + 32, sv[1]);
+          wait_ld_regs(sv[0], sv[1]);
+          tmem_ld32(s_addr + 64, sv[2]);
         }
+        // quarter c4's scores have arrived (or arrive now)
+        auto have = [&](int c4, bool again) {
+          if constexpr (!kSepP) {
+            if (c4 == 3 || (c4 == 2 && again)) tmem_ld32(s_addr + c4 * 32, sv[2]);
+            if (c4 >= 2) wait_ld_regs32(sv[2]);
+          }
+        };
         uint64_t ls0 = 0, ls1 = 0;
         float mq[4];
-        // O and the sum move to a new maximum (a block's first maximum needs no O yet)
+        // O and the sum move to a new maximum (before the first P V there is no O yet)
         auto rescale = [&](float m_new) {
           const float f = m_new == -INFINITY ? 1.0f : ex2(m_used - m_new);
           l *= f;
           if (j > 0) {
             tmem_st_wait();
 #pragma unroll 1
-            for (int cc = 0; cc < DH / 32; ++cc) {
-              uint32_t ov[32];
-              tmem_ld32(o_addr + cc * 32, ov);
+            for (int cc = 0; cc < DH / 16; ++cc) {
+              uint32_t ov[16];
+              tmem_ld16(o_addr + cc * 16, ov);
               tmem_ld_wait();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
-              tmem_st32(o_addr + cc * 32, ov);
+              for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+              tmem_st16(o_addr + cc * 16, ov);
             }
           }
           m_used = m_new;
         };
-        // P = exp2(x - m) over S.  The exponentials use the running maximum at once and the block's own maximum is
-        // taken alongside; if a row's grows by more than 2^8 the block is done again after O has been rescaled
-        // (rare).  Until then P <= 2^8, which bf16 and the fp32 sums hold.
-        auto fast = [&](bool with_max) {
+        // score k, k + 1 of a quarter relative to m; not seen: -infinity
+        auto score2 = [&](int c4, int k, uint64_t nm2, bool masked, float& x0, float& x1) {
+          uint64_t a2, b2, sp;
+          ld_shared_2x64(sc + (c4 * 16 + k) * 16, a2, b2);
+          asm("mov.b64 %0, {%1, %2};" : "=l"(sp) : "r"(sv[buf(c4)][2 * k]), "r"(sv[buf(c4)][2 * k + 1]));
+          unpack2(fma2(sp, a2, fma2(b2, qs2, nm2)), x0, x1);
+          if (masked) {
+            if (c4 * 32 + 2 * k >= left) x0 = -INFINITY;
+            if (c4 * 32 + 2 * k + 1 >= left) x1 = -INFINITY;
+          }
+        };
+        // P = exp2(x - m) over S, the sums, and (with_max) the largest x - m
+        auto exps = [&](bool with_max, bool masked, bool again) {
           const float nm = m_used == -INFINITY ? 0.0f : -m_used;
           const uint64_t nm2 = pack2(nm, nm);
           ls0 = 0;
@@ -548,16 +645,12 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
           for (int k = 0; k < 4; ++k) mq[k] = -INFINITY;
 #pragma unroll
           for (int c4 = 0; c4 < 4; ++c4) {
-            if (c4 == 2 && split_ld && with_max) wait_ld_regs(sv[2], sv[3]);
+            have(c4, again);
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              uint64_t a2, b2, xp, sp;
-              ld_shared_2x64(sc + (c4 * 16 + k) * 16, a2, b2);
-              asm("mov.b64 %0, {%1, %2};" : "=l"(sp) : "r"(sv[c4][2 * k]), "r"(sv[c4][2 * k + 1]));
-              xp = fma2(sp, a2, fma2(b2, qs2, nm2));
               float x0, x1;
-              unpack2(xp, x0, x1);
+              score2(c4, k, nm2, masked, x0, x1);
               if (with_max) mq[k & 3] = max3(mq[k & 3], x0, x1);
               const float p0 = ex2(x0), p1 = ex2(x1);
               if (k & 1) ls1 = add2(ls1, pack2(p0, p1));
@@ -568,46 +661,31 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
           }
         };
         if (!careful) {
-          fast(true);
-          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));  // relative to m_used
+          // The exponentials use the running maximum at once and the block's own maximum is taken alongside; if a
+          // row's grows by more than 2^8 the block is done again after O has been rescaled (rare).  Until then
+          // P <= 2^8, which bf16 and the fp32 sums hold.
+          exps(true, false, false);
+          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
           if (__any_sync(0xffffffffu, mx > 8.0f)) {
-            const float base = m_used == -INFINITY ? 0.0f : m_used;
-            rescale(fmaxf(m_used, base + mx));
-            fast(false);
+            rescale(fmaxf(m_used, (m_used == -INFINITY ? 0.0f : m_used) + mx));
+            exps(false, false, true);
           }
         } else {
-          // scores in place, those of keys that the row does not see at -infinity
 #pragma unroll
           for (int k = 0; k < 4; ++k) mq[k] = -INFINITY;
 #pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4)
+          for (int c4 = 0; c4 < 4; ++c4) {
+            have(c4, false);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              uint64_t a2, b2, sp;
-              ld_shared_2x64(sc + (c4 * 16 + k) * 16, a2, b2);
-              asm("mov.b64 %0, {%1, %2};" : "=l"(sp) : "r"(sv[c4][2 * k]), "r"(sv[c4][2 * k + 1]));
               float x0, x1;
-              unpack2(fma2(sp, a2, fma2(b2, qs2, 0)), x0, x1);
-              if (key0 + c4 * 32 + 2 * k >= lim) x0 = -INFINITY;
-              if (key0 + c4 * 32 + 2 * k + 1 >= lim) x1 = -INFINITY;
+              score2(c4, k, 0, true, x0, x1);
               mq[k & 3] = max3(mq[k & 3], x0, x1);
-              sv[c4][2 * k] = __float_as_uint(x0);
-              sv[c4][2 * k + 1] = __float_as_uint(x1);
             }
+          }
           const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
           if (__any_sync(0xffffffffu, mx > m_used + 8.0f)) rescale(fmaxf(m_used, mx));
-          const float nm = m_used == -INFINITY ? 0.0f : -m_used;
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float p0 = ex2(__uint_as_float(sv[c4][2 * k]) + nm), p1 = ex2(__uint_as_float(sv[c4][2 * k + 1]) + nm);
-              ls0 = add2(ls0, pack2(p0, p1));
-              pk[k] = pack_bf16x2(p0, p1);
-            }
-            tmem_st16(p_addr + c4 * 16, pk);
-          }
+          exps(false, true, true);
         }
         float la, lb;
         unpack2(add2(ls0, ls1), la, lb);
@@ -619,19 +697,19 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         ++n_sig;
       }
       if (!ok) break;
-      if (!(ok = mbar_wait(&unit_done[u], uph, ctl, 965))) break;
-      const bool poison = s_bad[u] < lim;  // the row sees a key whose V is not finite
+      if (!(ok = mbar_wait(&rec_v[rec], v_ph, ctl, 965))) break;
+      const bool poison = r->bad < lim;  // the row sees a key whose V is not finite
       if (!(ok = mbar_wait(&o_full[x], oph, ctl, 966))) break;
       oph ^= 1;
       tc_fence_after();
 
       // A unit cut by the border of a run: each part leaves its unnormalised O, maxima and sums and counts itself in;
       // the last one (it waits for nobody) merges all parts in their order.
-      const int cta0 = w.first_cta(), cta1 = w.last_cta(), slab = x * 4 + quarter;
+      const int cta0 = r->cta0, cta1 = r->cta1, slab = x * 4 + quarter;
       const float* parts = nullptr;
       if (cta0 != cta1) {
         constexpr int kSlab = many_slab<DH>();
-        float* mine = p.part + (((int64_t)blockIdx.x * 2 + (w.step == 0 ? 1 : 0)) * 8 + slab) * kSlab;
+        float* mine = p.part + (((int64_t)blockIdx.x * 2 + (step == 0 ? 1 : 0)) * 8 + slab) * kSlab;
 #pragma unroll 1
         for (int cc = 0; cc < DH / 32; ++cc) {  // [column/4][row][4]: each store a contiguous 512 bytes
           uint32_t ov[32];
@@ -655,7 +733,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         if (order != cta1 - cta0) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&o_empty[x]);
+          if (lane == 0) {
+            mbar_arrive(&o_empty[x]);
+            mbar_arrive(&rec_empty[rec]);
+          }
           continue;
         }
         __threadfence();
@@ -671,23 +752,23 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
       }
       // no key seen: O = 0, LSE = -inf.  Scores that are NaN leave l = NaN, and stay NaN.
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      // 32 columns at a time through this warp's slab of shared memory, out in rows of 64 bytes
+      // 16 columns at a time through this warp's slab of shared memory, out in whole 32-byte sectors
 #pragma unroll 1
-      for (int cc = 0; cc < DH / 32; ++cc) {
-        uint32_t ov[32];
+      for (int cc = 0; cc < DH / 16; ++cc) {
+        uint32_t ov[16];
         if (!parts) {
-          tmem_ld32(o_addr + cc * 32, ov);
+          tmem_ld16(o_addr + cc * 16, ov);
           tmem_ld_wait();
         } else {
           constexpr int kSlab = many_slab<DH>();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) ov[k] = 0;
+          for (int k = 0; k < 16; ++k) ov[k] = 0;
           for (int c = cta0; c <= cta1; ++c) {
             const float* src = parts + ((int64_t)(c - cta0) * 16 + (c == cta0 ? 8 : 0)) * kSlab;
             const float f = m_used == -INFINITY ? 1.0f : ex2(__ldcg(src + DH * 32 + lane) - m_used);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + ((cc * 8 + k) * 32 + lane) * 4));
+            for (int k = 0; k < 4; ++k) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(src + ((cc * 4 + k) * 32 + lane) * 4));
               ov[4 * k] = __float_as_uint(fmaf(f, v.x, __uint_as_float(ov[4 * k])));
               ov[4 * k + 1] = __float_as_uint(fmaf(f, v.y, __uint_as_float(ov[4 * k + 1])));
               ov[4 * k + 2] = __float_as_uint(fmaf(f, v.z, __uint_as_float(ov[4 * k + 2])));
@@ -698,24 +779,27 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         __syncwarp();  // the slab's last rows have been read
         const float scale = poison ? NAN : inv;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          st_shared_v4(stage + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4),
+        for (int k = 0; k < 2; ++k)
+          st_shared_v4(stage + lane * 32 + ((k ^ ((lane >> 2) & 1)) << 4),
                        pack_bf16x2(__uint_as_float(ov[8 * k]) * scale, __uint_as_float(ov[8 * k + 1]) * scale),
                        pack_bf16x2(__uint_as_float(ov[8 * k + 2]) * scale, __uint_as_float(ov[8 * k + 3]) * scale),
                        pack_bf16x2(__uint_as_float(ov[8 * k + 4]) * scale, __uint_as_float(ov[8 * k + 5]) * scale),
                        pack_bf16x2(__uint_as_float(ov[8 * k + 6]) * scale, __uint_as_float(ov[8 * k + 7]) * scale));
         __syncwarp();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = 8 * k + (int)(lane >> 2), to = __shfl_sync(0xffffffffu, at, row);
-          const uint4 v = ld_shared_v4(stage + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
-          if (to >= 0) st_global_v4(p.o + (size_t)to * DH + cc * 32 + (lane & 3) * 8, v.x, v.y, v.z, v.w);
+        for (int k = 0; k < 2; ++k) {
+          const int row = 16 * k + (int)(lane >> 1), to = __shfl_sync(0xffffffffu, at, row);
+          const uint4 v = ld_shared_v4(stage + row * 32 + (((lane & 1) ^ ((row >> 2) & 1)) << 4));
+          if (to >= 0) st_global_v4(p.o + (size_t)to * DH + cc * 16 + (lane & 1) * 8, v.x, v.y, v.z, v.w);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&o_empty[x]);
-      if (row_ok && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m_used + lg2(l)) * kLn2;
+      if (lane == 0) {
+        mbar_arrive(&o_empty[x]);
+        mbar_arrive(&rec_empty[rec]);
+      }
+      if (at >= 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m_used + lg2(l)) * kLn2;
     }
   }
 
