@@ -29,7 +29,7 @@ constexpr int kThreadsMany = 512, BM = 128, BN = 128;
 constexpr int kSoftWarp = 4, kDeqWarp = 12;
 constexpr int kRecs = 4;  // records of units on their way through the roles
 // 4 warpgroups launched at 128 registers a thread; the shares add up to what was launched
-constexpr uint32_t kLaunchRegs = 128, kRegsCtl = 64, kRegsDeq = 80, kRegsSoft = 184;
+constexpr uint32_t kLaunchRegs = 128, kRegsCtl = 104, kRegsDeq = 104, kRegsSoft = 152;
 static_assert(kRegsCtl + kRegsDeq + 2 * kRegsSoft == 4 * kLaunchRegs, "register split");
 
 // One unit's run of key blocks, as warp 2 hands it to the other roles.
@@ -67,20 +67,7 @@ struct ManySmem {
 template <int DH>
 constexpr int many_slab() { return 32 * (DH + 2); }  // floats of a partial result of 32 rows: O [dh/4][32][4], m, l
 
-__device__ __forceinline__ void wait_ld_regs(uint32_t (&a)[32], uint32_t (&b)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
-                 "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
-                 "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]), "+r"(a[22]), "+r"(a[23]),
-                 "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]), "+r"(a[31]),
-                 "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]),
-                 "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15]),
-                 "+r"(b[16]), "+r"(b[17]), "+r"(b[18]), "+r"(b[19]), "+r"(b[20]), "+r"(b[21]), "+r"(b[22]), "+r"(b[23]),
-                 "+r"(b[24]), "+r"(b[25]), "+r"(b[26]), "+r"(b[27]), "+r"(b[28]), "+r"(b[29]), "+r"(b[30]), "+r"(b[31])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void wait_ld_regs32(uint32_t (&a)[32]) {
+__device__ __forceinline__ void wait_ld_regs(uint32_t (&a)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
                  "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15]),
@@ -420,7 +407,11 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
     constexpr int PARTS = DH / 32;     // 16-byte parts of a row of codes
     constexpr int RPI = 32 / PARTS;    // rows of one load instruction
     constexpr int ITER = 32 / RPI;     // loads for this warp's 32 keys
-    const int dw = warp - kDeqWarp, part = lane % PARTS, sub = lane / PARTS;
+    // this lane's part of a row and row of a load: the 8 lanes of a 16-byte store's phase are four rows and the two parts
+    // of one 128-byte half, which the swizzle spreads over all banks
+    const int dw = warp - kDeqWarp;
+    const int part = DH == 128 ? (lane & 1) | ((lane >> 2) & 2) : lane & 1;
+    const int sub = DH == 128 ? ((lane >> 1) & 3) | ((lane >> 2) & 4) : lane >> 1;
     const uint32_t staging = smem_u32(smem + L::off_staging), scales = smem_u32(smem + L::off_scale), ring = smem_u32(s_ring);
     const float cl = p.scale_log2;
     uint32_t rs = 0, rph = 0, si = 0, sph = 0, kord = 0;
@@ -441,33 +432,24 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         const uint32_t src = staging + si * L::kStaging;
         uint32_t sc;
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc) : "r"(src + BN * (DH / 2) + (32 * dw + lane) * 4) : "memory");
-        uint4 c[ITER];
-#pragma unroll
-        for (int s = 0; s < ITER; ++s) c[s] = ld_shared_v4(src + (32 * dw + RPI * s + sub) * (DH / 2) + part * 16);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&st_empty[si]);
         if ((int)lane >= left) sc = 0;  // places past the history: codes are always finite, a zero step makes zeros of V
         if (!(ok = mbar_wait(&ring_empty[rs], rph ^ 1, ctl, 958))) break;
-        const uint32_t slot = ring + rs * L::kTile + (part >> 1) * (BN * 128);
-        // Bank conflicts: 8 lanes of a store are two rows times four parts; parts 2 and 3 are in another chunk of 64
-        // channels at the same banks, and take their words in another order
-        const uint32_t swap = (part >> 1) << 1;
+        const uint32_t slot = ring + rs * L::kTile + (part >> 1) * (BN * 128) + (32 * dw + sub) * 128;
+        const uint32_t codes = src + (32 * dw + sub) * (DH / 2) + part * 16;
         if (!v) {
           // a and b of this lane's key, in pairs {a0, a1, b0, b1}
           const uint32_t at = scales + (kord % L::kScales) * (BN * 8) + (16 * dw + (lane >> 1)) * 16 + (lane & 1) * 4;
           const float a = cl * bf_lo(sc), b = fmaf(-16.0f, a, cl * bf_hi(sc));
           st_shared_u32(at, __float_as_uint(a));
           st_shared_u32(at + 8, __float_as_uint(b));
-#pragma unroll
+#pragma unroll 1
           for (int s = 0; s < ITER; ++s) {
-            const int row = 32 * dw + RPI * s + sub;
-            const uint32_t cw[4] = {c[s].x, c[s].y, c[s].z, c[s].w};
+            const uint4 c = ld_shared_v4(codes + s * RPI * (DH / 2));
+            const uint32_t cw[4] = {c.x, c.y, c.z, c.w}, sw = (RPI * s + sub) & 7;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t x = swap ? cw[k ^ 2] : cw[k];
-              st_shared_v4(slot + row * 128 + (((((part & 1) << 2) | (k ^ swap)) ^ (row & 7)) << 4), pair16<0>(x), pair16<1>(x),
-                           pair16<2>(x), pair16<3>(x));
-            }
+            for (int k = 0; k < 4; ++k)
+              st_shared_v4(slot + s * RPI * 128 + ((((part & 1) << 2 | k) ^ sw) << 4), pair16<0>(cw[k]), pair16<1>(cw[k]), pair16<2>(cw[k]),
+                           pair16<3>(cw[k]));
           }
         } else {
           // a row with values that are not finite: zeros here, and NaN for the rows that see it (in the epilogue)
@@ -477,23 +459,22 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
             if (lane == 0) atomicMin(const_cast<int*>(&recs[rec].bad), key0 + __ffs(any) - 1);
             if (bad) sc = 0;
           }
-#pragma unroll
+#pragma unroll 1
           for (int s = 0; s < ITER; ++s) {
-            const int row = 32 * dw + RPI * s + sub;
-            const uint32_t cw[4] = {c[s].x, c[s].y, c[s].z, c[s].w};
+            const uint4 c = ld_shared_v4(codes + s * RPI * (DH / 2));
+            const uint32_t cw[4] = {c.x, c.y, c.z, c.w}, sw = (RPI * s + sub) & 7;
             const uint32_t rsc = __shfl_sync(0xffffffffu, sc, RPI * s + sub);
             const uint32_t st2 = __byte_perm(rsc, rsc, 0x1010), mn2 = __byte_perm(rsc, rsc, 0x3232);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t x = swap ? cw[k ^ 2] : cw[k];
-              st_shared_v4(slot + row * 128 + (((((part & 1) << 2) | (k ^ swap)) ^ (row & 7)) << 4), value2(pair16<0>(x), st2, mn2),
-                           value2(pair16<1>(x), st2, mn2), value2(pair16<2>(x), st2, mn2), value2(pair16<3>(x), st2, mn2));
-            }
+            for (int k = 0; k < 4; ++k)
+              st_shared_v4(slot + s * RPI * 128 + ((((part & 1) << 2 | k) ^ sw) << 4), value2(pair16<0>(cw[k]), st2, mn2),
+                           value2(pair16<1>(cw[k]), st2, mn2), value2(pair16<2>(cw[k]), st2, mn2), value2(pair16<3>(cw[k]), st2, mn2));
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
+          mbar_arrive(&st_empty[si]);
           if (!v) mbar_arrive(&sc_full[kord % L::kScales]);
           if (i == 2 * n - 1) mbar_arrive(&rec_v[rec]);
           mbar_arrive(&ring_full[rs]);
@@ -571,125 +552,104 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         if (!(ok = mbar_wait(&s_full[x], sph, ctl, 963))) break;
         sph ^= 1;
         tc_fence_after();
-        const int left = lim - (step + j) * BN;  // keys of the block that the row sees
-        const bool careful = j == 0 || (step + j + 1) * BN > lim_min;  // a first block, or one that some row does not see all of
-        // Scores in quarters of 32.  With P over S (dh = 128) P of quarter c lies over quarter c / 2, so quarters in
-        // order never overwrite an unread one; the first two stay in registers for the case that the block is done
-        // again, the last two can be read again.  With P apart all of S is read at once, and the next S may come.
-        constexpr int kBuf = kSepP ? 4 : 3;
-        uint32_t sv[kBuf][32];
-        auto buf = [](int c4) { return c4 < kBuf ? c4 : kBuf - 1; };
-        if constexpr (kSepP) {
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(s_addr + c4 * 32, sv[c4]);
-          wait_ld_regs(sv[0], sv[1]);
-          wait_ld_regs(sv[2], sv[3]);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[x]);
-          if (n_sig > 0) {  // P is rewritten, and O rescaled, only after the last P V
-            if (!(ok = mbar_wait(&pv_done[x], (n_sig - 1) & 1, ctl, 964))) break;
-            tc_fence_after();
-          }
-        } else {
-          tmem_ld32(s_addr, sv[0]);
-          tmem_ld32(s_addr + 32, sv[1]);
-          wait_ld_regs(sv[0], sv[1]);
-          tmem_ld32(s_addr + 64, sv[2]);
-        }
-        // quarter c4's scores have arrived (or arrive now)
-        auto have = [&](int c4, bool again) {
-          if constexpr (!kSepP) {
-            if (c4 == 3 || (c4 == 2 && again)) tmem_ld32(s_addr + c4 * 32, sv[2]);
-            if (c4 >= 2) wait_ld_regs32(sv[2]);
-          }
-        };
-        uint64_t ls0 = 0, ls1 = 0;
-        float mq[4];
-        // O and the sum move to a new maximum (before the first P V there is no O yet)
-        auto rescale = [&](float m_new) {
-          const float f = m_new == -INFINITY ? 1.0f : ex2(m_used - m_new);
-          l *= f;
-          if (j > 0) {
-            tmem_st_wait();
+        const int left = lim - (step + j) * BN;            // keys of the block that the row sees
+        const bool cut = (step + j + 1) * BN > lim_min;   // some row does not see all of the block
+        // P = exp2(x - m) in quarters of 32 keys, in a rolled loop: unrolled, the code of the roles together does not
+        // fit the instruction cache.  With P over S (dh = 128) P of quarter c lies over quarter c / 2 of S, so quarters
+        // in order never overwrite an unread one.  The exponentials use the running maximum m at once and the
+        // quarter's own maximum is taken alongside; where a row's grows by more than 2^8 (rare) m moves up by a whole
+        // number, so that what has been summed so far is scaled by a power of two, exactly.  Until then P <= 2^8,
+        // which bf16 and the fp32 sums hold.
+        uint32_t s[32];
+        tmem_ld32(s_addr, s);
 #pragma unroll 1
-            for (int cc = 0; cc < DH / 16; ++cc) {
-              uint32_t ov[16];
-              tmem_ld16(o_addr + cc * 16, ov);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
-              tmem_st16(o_addr + cc * 16, ov);
-            }
-          }
-          m_used = m_new;
-        };
-        // score k, k + 1 of a quarter relative to m; not seen: -infinity
-        auto score2 = [&](int c4, int k, uint64_t nm2, bool masked, float& x0, float& x1) {
-          uint64_t a2, b2, sp;
-          ld_shared_2x64(sc + (c4 * 16 + k) * 16, a2, b2);
-          asm("mov.b64 %0, {%1, %2};" : "=l"(sp) : "r"(sv[buf(c4)][2 * k]), "r"(sv[buf(c4)][2 * k + 1]));
-          unpack2(fma2(sp, a2, fma2(b2, qs2, nm2)), x0, x1);
-          if (masked) {
-            if (c4 * 32 + 2 * k >= left) x0 = -INFINITY;
-            if (c4 * 32 + 2 * k + 1 >= left) x1 = -INFINITY;
-          }
-        };
-        // P = exp2(x - m) over S, the sums, and (with_max) the largest x - m
-        auto exps = [&](bool with_max, bool masked, bool again) {
+        for (int c4 = 0; c4 < 4; ++c4) {
           const float nm = m_used == -INFINITY ? 0.0f : -m_used;
           const uint64_t nm2 = pack2(nm, nm);
-          ls0 = 0;
-          ls1 = 0;
+          float xs[32], mq[4];
+          wait_ld_regs(s);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            uint64_t a2, b2, sp;
+            ld_shared_2x64(sc + (c4 * 16 + k) * 16, a2, b2);
+            asm("mov.b64 %0, {%1, %2};" : "=l"(sp) : "r"(s[2 * k]), "r"(s[2 * k + 1]));
+            unpack2(fma2(sp, a2, fma2(b2, qs2, nm2)), xs[2 * k], xs[2 * k + 1]);
+          }
+          if (c4 < 3) tmem_ld32(s_addr + (c4 + 1) * 32, s);
+          else if (kSepP) {  // S is in registers: the next one may come
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[x]);
+          }
+          if (cut) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c4 * 32 + k >= left) xs[k] = -INFINITY;
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k) mq[k] = -INFINITY;
 #pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
-            have(c4, again);
-            uint32_t pk[16];
+          for (int k = 0; k < 16; ++k) mq[k & 3] = max3(mq[k & 3], xs[2 * k], xs[2 * k + 1]);
+          uint32_t pk[16];
+          uint64_t ls0, ls1;
+          auto exps = [&]() {
+            ls0 = ls1 = 0;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              float x0, x1;
-              score2(c4, k, nm2, masked, x0, x1);
-              if (with_max) mq[k & 3] = max3(mq[k & 3], x0, x1);
-              const float p0 = ex2(x0), p1 = ex2(x1);
+              const float p0 = ex2(xs[2 * k]), p1 = ex2(xs[2 * k + 1]);
               if (k & 1) ls1 = add2(ls1, pack2(p0, p1));
               else ls0 = add2(ls0, pack2(p0, p1));
               pk[k] = pack_bf16x2(p0, p1);
             }
-            tmem_st16(p_addr + c4 * 16, pk);
+          };
+          exps();
+          if (kSepP && c4 == 0 && n_sig > 0) {  // P is rewritten, and O rescaled, only after the last P V
+            if (!(ok = mbar_wait(&pv_done[x], (n_sig - 1) & 1, ctl, 964))) break;
+            tc_fence_after();
           }
-        };
-        if (!careful) {
-          // The exponentials use the running maximum at once and the block's own maximum is taken alongside; if a
-          // row's grows by more than 2^8 the block is done again after O has been rescaled (rare).  Until then
-          // P <= 2^8, which bf16 and the fp32 sums hold.
-          exps(true, false, false);
           const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-          if (__any_sync(0xffffffffu, mx > 8.0f)) {
-            rescale(fmaxf(m_used, (m_used == -INFINITY ? 0.0f : m_used) + mx));
-            exps(false, false, true);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mq[k] = -INFINITY;
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) {
-            have(c4, false);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float x0, x1;
-              score2(c4, k, 0, true, x0, x1);
-              mq[k & 3] = max3(mq[k & 3], x0, x1);
+          if (__any_sync(0xffffffffu, mx > (m_used == -INFINITY ? -INFINITY : 8.0f))) {
+            float up = 0.0f, f = 1.0f;
+            if (m_used == -INFINITY) {  // first keys that the row sees: nothing has been summed
+              if (mx > -INFINITY) {
+                m_used = up = mx;
+                f = 0.0f;
+              }
+            } else if (mx > 8.0f) {
+              up = ceilf(mx);
+              m_used += up;
+              f = ex2(-up);
             }
+            l *= f;
+            tmem_st_wait();
+            if (j > 0) {  // before the first P V there is no O
+#pragma unroll 1
+              for (int cc = 0; cc < DH / 16; ++cc) {
+                tmem_ld16(o_addr + cc * 16, pk);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) pk[k] = __float_as_uint(__uint_as_float(pk[k]) * f);
+                tmem_st16(o_addr + cc * 16, pk);
+              }
+            }
+#pragma unroll 1
+            for (int cc = 0; cc < c4; ++cc) {  // the block's earlier quarters of P
+              tmem_ld16(p_addr + cc * 16, pk);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) pk[k] = pack_bf16x2(bf_lo(pk[k]) * f, bf_hi(pk[k]) * f);
+              tmem_st16(p_addr + cc * 16, pk);
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) xs[k] -= up;
+            exps();
           }
-          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-          if (__any_sync(0xffffffffu, mx > m_used + 8.0f)) rescale(fmaxf(m_used, mx));
-          exps(false, true, true);
+          float la, lb;
+          unpack2(add2(ls0, ls1), la, lb);
+          l += la + lb;
+          tmem_st16(p_addr + c4 * 16, pk);
         }
-        float la, lb;
-        unpack2(add2(ls0, ls1), la, lb);
-        l += la + lb;
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
