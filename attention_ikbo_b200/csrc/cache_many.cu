@@ -5,10 +5,14 @@
 // Each 4-bit value is used by up to 256 rows, so the tensor core and the exponentials bound it.  Per K/V block of 128
 // keys, from L2 once for both 128-row query tiles:
 //   * K goes to the tensor core as 16 + c, exact in bf16 (four mantissa bits under a leading one; a shift and one logic
-//     operation for two values), and the softmax applies the key's step and minimum to the fp32 product,
-//         x_ij = a_j (q_i . (16 + c_j)) + b_j sum(q_i),   a_j = sK_j scale log2(e),  b_j = (mK_j - 16 sK_j) scale log2(e),
-//     two packed FMAs for two scores where a plain softmax has one: scores are exact up to fp32 sums.  Rounding the
-//     keys to bf16 instead would put 2^-9 of every product into the scores.
+//     operation for two values).  With t_j = mK_j / sK_j - 16 the score is
+//         x_ij = a_j (q_i . (16 + c_j) + t_j sum(q_i)),   a_j = sK_j scale log2(e).
+//     The product t_j sum(q_i) is one more contraction step of the tensor core: both factors in three bf16 parts (24
+//     bits), the six products that matter in six of its 16 columns.  So the softmax has one packed FMA for two scores,
+//     as one without codes would have, and scores are exact up to fp32 sums.  Applying the minimum in the softmax
+//     instead, a second packed FMA and twice the shared-memory reads, took 1016 us where this takes LONGUS (8 histories
+//     of 4096-8192 keys, 4 heads, 8192 rows each); rounding the keys to bf16 would put 2^-9 of every product into the
+//     scores.
 //   * V is rounded to bf16 once, as P is and as the output is: its error is a weighted mean of such roundings.
 // Warp roles (512 threads): warp 0 loads query tiles by TMA, warp 1 issues tcgen05.mma, warp 2 walks the work and copies
 // codes, steps and minima into staging buffers (cp.async.bulk, one copy for each page), warps 4-7 and 8-11 are the
@@ -29,7 +33,7 @@ constexpr int kThreadsMany = 512, BM = 128, BN = 128;
 constexpr int kSoftWarp = 4, kDeqWarp = 12;
 constexpr int kRecs = 4;  // records of units on their way through the roles
 // 4 warpgroups launched at 128 registers a thread; the shares add up to what was launched
-constexpr uint32_t kLaunchRegs = 128, kRegsCtl = 104, kRegsDeq = 104, kRegsSoft = 152;
+constexpr uint32_t kLaunchRegs = 128, kRegsCtl = 64, kRegsDeq = 64, kRegsSoft = 192;
 static_assert(kRegsCtl + kRegsDeq + 2 * kRegsSoft == 4 * kLaunchRegs, "register split");
 
 // One unit's run of key blocks, as warp 2 hands it to the other roles.
@@ -47,26 +51,29 @@ struct ManySmem {
   static constexpr int kRing = DH == 128 ? 4 : 6;
   static constexpr int kStaged = DH == 128 ? 2 : 4;
   static constexpr uint32_t kStaging = BN * DH / 2 + BN * 4;  // codes, then steps and minima
-  // Steps and minima of a K block stay until both tiles' softmax is done with it.  A block is converted once the ring
-  // slot kRing items before it is free.  At dh = 128 that item is at the earliest the K block before the last, whose S
-  // was issued after P of the block before it: four slots are enough.  At dh = 64 S runs ahead of P: eight.
+  // A K block's a and t: a block is converted once the ring slot kRing items before it is free, at the earliest that of
+  // the K block before the last (dh = 64: the one before that), whose S was issued after P of the block before it: four
+  // (eight) slots are enough for both tiles' softmax to be done with the old one.
   static constexpr int kScales = DH == 128 ? 4 : 8;
-  static constexpr uint32_t kOut = 32 * 32;       // per softmax warp: 32 rows x 16 columns of O (bf16)
+  static constexpr uint32_t kAug = BM * 16;       // 8 columns of the extra contraction step; the other 8 are zeros
   static constexpr uint32_t off_q = 0;
   static constexpr uint32_t off_ring = 2 * kTile;
   static constexpr uint32_t off_staging = off_ring + kRing * kTile;
-  static constexpr uint32_t off_out = off_staging + kStaged * kStaging;
-  static constexpr uint32_t off_scale = off_out + 8 * kOut;  // kScales x 64 key pairs x {a0, a1, b0, b1}
-  static constexpr uint32_t off_rec = off_scale + kScales * BN * 8;
+  static constexpr uint32_t off_aug_q = off_staging + kStaged * kStaging;
+  static constexpr uint32_t off_aug_k = off_aug_q + 2 * kAug;
+  static constexpr uint32_t off_zero = off_aug_k + kScales * kAug;
+  static constexpr uint32_t off_scale = off_zero + kAug;  // kScales x 128 x a
+  static constexpr uint32_t off_rec = off_scale + kScales * BN * 4;
   static constexpr uint32_t off_bar = off_rec + kRecs * sizeof(Rec);
-  static constexpr uint32_t n_bars = 2 * kRing + 2 * 8 + 1 + kScales + 3 * kRecs + 2 * kStaged;
+  static constexpr uint32_t n_bars = 2 * kRing + 2 * 7 + 1 + kScales + 3 * kRecs + 2 * kStaged;
   static constexpr uint32_t off_misc = off_bar + n_bars * 8;
   static constexpr uint32_t alloc_bytes = off_misc + 16 + 1024;
-  static_assert(alloc_bytes <= 232448 - 512, "shared memory budget");
+  static_assert(alloc_bytes <= 232448 - 288, "shared memory budget");
 };
 template <int DH>
 constexpr int many_slab() { return 32 * (DH + 2); }  // floats of a partial result of 32 rows: O [dh/4][32][4], m, l
 
+// tcgen05.wait::ld that names the loaded registers, so that no use of them moves before it
 __device__ __forceinline__ void wait_ld_regs(uint32_t (&a)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
@@ -91,6 +98,19 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+// operand descriptor without swizzle, K-major: 8-row groups of 16-byte rows 128 bytes apart, the second 8 columns lbo on
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t saddr, uint32_t lbo) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
+}
+// x in three bf16 parts, most significant first, as bits
+__device__ __forceinline__ void split3(float x, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const __nv_bfloat16 h = __float2bfloat16_rn(x);
+  const float r = x - __bfloat162float(h);
+  const __nv_bfloat16 m = __float2bfloat16_rn(r), l = __float2bfloat16_rn(r - __bfloat162float(m));
+  a = __bfloat16_as_ushort(h);
+  b = __bfloat16_as_ushort(m);
+  c = __bfloat16_as_ushort(l);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
@@ -122,14 +142,13 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
   uint64_t* ring_full = bars;
   uint64_t* ring_empty = bars + kRing;
   uint64_t* q_full = bars + 2 * kRing;  // [2] query tile landed
-  uint64_t* q_empty = q_full + 2;       // [2] its last S computed and its rows' sums taken
+  uint64_t* q_empty = q_full + 2;       // [2] its last S computed
   uint64_t* s_full = q_empty + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_full = p_full + 2;
   uint64_t* o_empty = o_full + 2;
-  uint64_t* s_free = o_empty + 2;    // [2] separate P: S read into registers
-  uint64_t* pv_done = s_free + 2;    // [2] separate P: P V complete (P may be rewritten)
-  uint64_t* drain_bar = pv_done + 2;
+  uint64_t* qa_full = o_empty + 2;   // [2] the query rows' sums are there
+  uint64_t* drain_bar = qa_full + 2;
   uint64_t* sc_full = drain_bar + 1;           // [kScales] steps and minima of a K block are there
   uint64_t* rec_full = sc_full + L::kScales;   // [kRecs]
   uint64_t* rec_empty = rec_full + kRecs;      // [kRecs] read by every role, and the unit's epilogues done
@@ -155,13 +174,12 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&q_full[x], 1);
-      mbar_init(&q_empty[x], 1 + 4);
+      mbar_init(&q_empty[x], 1);
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
       mbar_init(&o_empty[x], 4);
-      mbar_init(&s_free[x], 4);
-      mbar_init(&pv_done[x], 1);
+      mbar_init(&qa_full[x], 4);
     }
     mbar_init(drain_bar, 1);
     for (int k = 0; k < L::kScales; ++k) mbar_init(&sc_full[k], 4);
@@ -177,10 +195,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
     *s_abort = 0;
     fence_mbar_init();
   }
-  if (tile_rows < BM) {  // rows that no query token fills
+  if (tile_rows < BM)  // rows that no query token fills
     for (uint32_t i = threadIdx.x; i < 2 * L::kTile / 16; i += kThreadsMany) reinterpret_cast<uint4*>(s_q)[i] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-  }
+  if (threadIdx.x < L::kAug / 16) reinterpret_cast<uint4*>(smem + L::off_zero)[threadIdx.x] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   if (warp == 1) {
     tmem_alloc(s_tmem, 512);
     tmem_relinquish();
@@ -189,11 +207,8 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
-  // TMEM columns: S_A [0,128) S_B [128,256) O_A [256,256+DH) O_B [256+DH,256+2DH).  dh = 128: P_X over S_X [0,64), so S
-  // of the next block waits for P V.  dh = 64 leaves 128 columns free: P_A [384,448), P_B [448,512) of their own.
-  constexpr bool kSepP = 256 + 2 * DH + 128 <= 512;
-  constexpr uint32_t kPCol = 256 + 2 * DH;
-
+  // TMEM columns: S_A [0,128) S_B [128,256) O_A [256,256+DH) O_B [256+DH,256+2DH); P_X over S_X [0,64), so S of the next
+  // block waits for P V.
   int ri = 0;
   uint32_t rec_ph = 0;  // this role's place among the unit records
   // the next unit's record; null after the last one, or when a wait has run out
@@ -307,10 +322,11 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
       // ------------------------------------------------------------------ tcgen05 issuer
       constexpr uint32_t idesc_s = idesc_bf16(BM, BN, false, false);  // S = Q (16 + c)^T: both K-major
       constexpr uint32_t idesc_o = idesc_bf16(BM, DH, false, true);   // O += P V: V is MN-major
-      uint32_t rs = 0, rph = 0, qph = 0, pph = 0, oeph = 0, sfph = 0;  // phase bits of the two tiles
-      bool s_pend[2] = {false, false};
+      uint32_t rs = 0, rph = 0, qph = 0, pph = 0, oeph = 0;  // phase bits of the two tiles
+      uint32_t kord = 0;
       bool ok = true;
-      const uint32_t q0 = smem_u32(s_q), ring0 = smem_u32(s_ring);
+      const uint32_t q0 = smem_u32(s_q), ring0 = smem_u32(s_ring), aug_q = smem_u32(smem + L::off_aug_q);
+      const uint32_t aug_k = smem_u32(smem + L::off_aug_k), zero = smem_u32(smem + L::off_zero);
       uint32_t slot = 0;
       auto take = [&](int where) -> bool {  // the next ring slot, in order of use
         if (!mbar_wait(&ring_full[rs], rph, ctl, where)) return false;
@@ -319,22 +335,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         tc_fence_after();
         return true;
       };
-      auto issue_s = [&](int x) -> bool {
-        if (kSepP) {
-          if (s_pend[x]) {
-            if (!mbar_wait(&s_free[x], (sfph >> x) & 1, ctl, 942)) return false;
-            sfph ^= 1u << x;
-            tc_fence_after();
-          }
-          s_pend[x] = true;
-        }
+      auto issue_s = [&](int x) {
         const uint64_t ad = sdesc_sw128(q0 + x * L::kTile, 16, 1024), bd = sdesc_sw128(ring0 + slot * L::kTile, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < DH / 16; ++kk)
           umma_ss(tmem_base + x * 128, sdesc_add(ad, (kk >> 2) * (BM * 128) + (kk & 3) * 32),
                   sdesc_add(bd, (kk >> 2) * (BN * 128) + (kk & 3) * 32), idesc_s, kk != 0);
+        const uint32_t qa = aug_q + x * L::kAug, ka = aug_k + (kord % L::kScales) * L::kAug;
+        umma_ss(tmem_base + x * 128, sdesc_plain(qa, zero - qa), sdesc_plain(ka, zero - ka), idesc_s, 1u);
         umma_commit(&s_full[x]);
-        return true;
       };
       auto issue_pv = [&](int x, uint32_t vslot, bool first) -> bool {
         if (!mbar_wait(&p_full[x], (pph >> x) & 1, ctl, 943)) return false;
@@ -345,11 +354,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         }
         tc_fence_after();
         const uint64_t vd = sdesc_sw128(ring0 + vslot * L::kTile, BN * 128, 1024);
-        const uint32_t pa = tmem_base + (kSepP ? kPCol + x * 64 : x * 128);
+        const uint32_t pa = tmem_base + x * 128;
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
           umma_ts(tmem_base + 256 + x * DH, pa + kk * 8, sdesc_add(vd, kk * 2048), idesc_o, (!first || kk != 0) ? 1u : 0u);
-        if (kSepP) umma_commit(&pv_done[x]);
         return true;
       };
       while (volatile Rec* r = next_rec(955)) {
@@ -358,34 +366,26 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         rec_step();
         if (keys == 0) continue;
         for (int x = 0; x < nx && ok; ++x) {
-          ok = mbar_wait(&q_full[x], (qph >> x) & 1, ctl, 945);
+          ok = mbar_wait(&q_full[x], (qph >> x) & 1, ctl, 945) && mbar_wait(&qa_full[x], (qph >> x) & 1, ctl, 947);
           qph ^= 1u << x;
         }
         if (!ok || !(ok = take(946))) break;
-        for (int x = 0; x < nx && ok; ++x) ok = issue_s(x);
-        if (!ok) break;
+        for (int x = 0; x < nx; ++x) issue_s(x);
         umma_commit(&ring_empty[slot]);
-        for (int j = 1; j < n && ok; ++j) {
+        ++kord;
+        for (int j = 1; j < n && ok; ++j, ++kord) {
           if (!(ok = take(948))) break;
           const uint32_t kslot = slot;
-          if (kSepP) {  // S of the next block as soon as the softmax has read the current one, then P V
-            for (int x = 0; x < nx && ok; ++x) ok = issue_s(x);
-            if (!ok) break;
-            umma_commit(&ring_empty[kslot]);
-            if (!(ok = take(949))) break;
-            const uint32_t vslot = slot;
-            for (int x = 0; x < nx && ok; ++x) ok = issue_pv(x, vslot, j == 1);
-            if (!ok) break;
-            umma_commit(&ring_empty[vslot]);
-          } else {
-            if (!(ok = take(949))) break;
-            const uint32_t vslot = slot;
-            slot = kslot;
-            for (int x = 0; x < nx && ok; ++x) ok = issue_pv(x, vslot, j == 1) && issue_s(x);
-            if (!ok) break;
-            umma_commit(&ring_empty[kslot]);
-            umma_commit(&ring_empty[vslot]);
+          if (!(ok = take(949))) break;
+          const uint32_t vslot = slot;
+          slot = kslot;
+          for (int x = 0; x < nx && ok; ++x) {
+            ok = issue_pv(x, vslot, j == 1);
+            if (ok) issue_s(x);
           }
+          if (!ok) break;
+          umma_commit(&ring_empty[kslot]);
+          umma_commit(&ring_empty[vslot]);
         }
         if (!ok) break;
         for (int x = 0; x < nx; ++x) umma_commit(&q_empty[x]);
@@ -414,12 +414,13 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
     const int sub = DH == 128 ? ((lane >> 1) & 3) | ((lane >> 2) & 4) : lane >> 1;
     const uint32_t staging = smem_u32(smem + L::off_staging), scales = smem_u32(smem + L::off_scale), ring = smem_u32(s_ring);
     const float cl = p.scale_log2;
-    uint32_t rs = 0, rph = 0, si = 0, sph = 0, kord = 0;
+    uint32_t rs = 0, rph = 0, si = 0, sph = 0, kord = 0, qph = 0;
+    const int trow = 32 * dw + (int)lane;
     bool ok = true;
     while (ok) {
       volatile Rec* r = next_rec(956);
       if (!r) break;
-      const int step = r->step, n = r->n, keys = r->L, rec = ri;
+      const int step = r->step, n = r->n, keys = r->L, rec = ri, nx = r->row0 + tile_rows < r->rows ? 2 : 1;
       __syncwarp();
       if (lane == 0) mbar_arrive(&rec_empty[ri]);
       rec_step();
@@ -437,11 +438,16 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         const uint32_t slot = ring + rs * L::kTile + (part >> 1) * (BN * 128) + (32 * dw + sub) * 128;
         const uint32_t codes = src + (32 * dw + sub) * (DH / 2) + part * 16;
         if (!v) {
-          // a and b of this lane's key, in pairs {a0, a1, b0, b1}
-          const uint32_t at = scales + (kord % L::kScales) * (BN * 8) + (16 * dw + (lane >> 1)) * 16 + (lane & 1) * 4;
-          const float a = cl * bf_lo(sc), b = fmaf(-16.0f, a, cl * bf_hi(sc));
-          st_shared_u32(at, __float_as_uint(a));
-          st_shared_u32(at + 8, __float_as_uint(b));
+          // a and t of this lane's key.  A step of zero, or too small to count beside its minimum, is taken as a tiny one:
+          // then t carries the minimum alone.
+          float st = bf_lo(sc);
+          const float mn = bf_hi(sc), least = fmaxf(fabsf(mn) * 8.673617e-19f, 7.888609e-31f);  // 2^-60, 2^-100
+          if (fabsf(st) < least) st = least;
+          uint32_t t1, t2, t3;
+          split3(mn / st - 16.0f, t1, t2, t3);
+          st_shared_u32(scales + ((kord % L::kScales) * BN + trow) * 4, __float_as_uint(cl * st));
+          st_shared_v4(smem_u32(smem + L::off_aug_k) + (kord % L::kScales) * L::kAug + trow * 16, t1 | t2 << 16, t3 | t1 << 16,
+                       t2 | t1 << 16, 0u);
 #pragma unroll 1
           for (int s = 0; s < ITER; ++s) {
             const uint4 c = ld_shared_v4(codes + s * RPI * (DH / 2));
@@ -482,6 +488,28 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         if (!v) ++kord;
         if (++rs == kRing) { rs = 0; rph ^= 1; }
         if (++si == L::kStaged) { si = 0; sph ^= 1; }
+        if (i > 0) continue;
+        // after a unit's first K block: sums of the query rows, the other factor of the extra contraction step
+        for (int x = 0; x < nx && ok; ++x) {
+          if (!(ok = mbar_wait(&q_full[x], (qph >> x) & 1, ctl, 959))) break;
+          qph ^= 1u << x;
+          const uint32_t qrow = smem_u32(s_q) + x * L::kTile + trow * 128;
+          float qs = 0.0f;
+#pragma unroll 1
+          for (int cc = 0; cc < DH / 64; ++cc)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint4 u = ld_shared_v4(qrow + cc * (BM * 128) + ((k ^ (trow & 7)) << 4));
+              qs += ((bf_lo(u.x) + bf_hi(u.x)) + (bf_lo(u.y) + bf_hi(u.y))) + ((bf_lo(u.z) + bf_hi(u.z)) + (bf_lo(u.w) + bf_hi(u.w)));
+            }
+          uint32_t q1, q2, q3;
+          split3(qs, q1, q2, q3);
+          st_shared_v4(smem_u32(smem + L::off_aug_q) + x * L::kAug + trow * 16, q1 | q1 << 16, q1 | q2 << 16, q2 | q3 << 16, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&qa_full[x]);
+        }
+        if (!ok) break;
       }
     }
   } else {
@@ -491,13 +519,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
     const int quarter = warp & 3;           // TMEM lanes 32*quarter .. +31
     const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
     const uint32_t s_addr = tmem_base + t_lane + x * 128;
-    const uint32_t p_addr = kSepP ? tmem_base + t_lane + kPCol + x * 64 : s_addr;
     const uint32_t o_addr = tmem_base + t_lane + 256 + x * DH;
-    const uint32_t stage = smem_u32(smem + L::off_out) + (warp - kSoftWarp) * L::kOut;
     const uint32_t scales = smem_u32(smem + L::off_scale);
     const int trow = 32 * quarter + (int)lane;
-    const uint32_t qrow = smem_u32(s_q) + x * L::kTile + trow * 128;
-    uint32_t kord = 0, qph = 0, sph = 0, oph = 0, n_sig = 0;
+    uint32_t kord = 0, sph = 0, oph = 0;
     bool ok = true;
     while (ok) {
       volatile Rec* const r = next_rec(960);
@@ -530,131 +555,140 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         continue;
       }
       const int lim_min = __reduce_min_sync(0xffffffffu, lim);
-      // sum of the row's query values
-      if (!(ok = mbar_wait(&q_full[x], qph, ctl, 961))) break;
-      qph ^= 1;
-      float qs = 0.0f;
-#pragma unroll
-      for (int cc = 0; cc < DH / 64; ++cc)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint4 v = ld_shared_v4(qrow + cc * (BM * 128) + ((k ^ (trow & 7)) << 4));
-          qs += ((bf_lo(v.x) + bf_hi(v.x)) + (bf_lo(v.y) + bf_hi(v.y))) + ((bf_lo(v.z) + bf_hi(v.z)) + (bf_lo(v.w) + bf_hi(v.w)));
-        }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_empty[x]);
-      const uint64_t qs2 = pack2(qs, qs);
-
       float m_used = -INFINITY, l = 0.0f;
       for (int j = 0; j < n; ++j, ++kord) {
-        const uint32_t sc = scales + (kord % L::kScales) * (BN * 8);
+        const uint32_t sc = scales + (kord % L::kScales) * (BN * 4);
         if (!(ok = mbar_wait(&sc_full[kord % L::kScales], (kord / L::kScales) & 1, ctl, 962))) break;
         if (!(ok = mbar_wait(&s_full[x], sph, ctl, 963))) break;
         sph ^= 1;
         tc_fence_after();
         const int left = lim - (step + j) * BN;            // keys of the block that the row sees
         const bool cut = (step + j + 1) * BN > lim_min;   // some row does not see all of the block
-        // P = exp2(x - m) in quarters of 32 keys, in a rolled loop: unrolled, the code of the roles together does not
-        // fit the instruction cache.  With P over S (dh = 128) P of quarter c lies over quarter c / 2 of S, so quarters
-        // in order never overwrite an unread one.  The exponentials use the running maximum m at once and the
-        // quarter's own maximum is taken alongside; where a row's grows by more than 2^8 (rare) m moves up by a whole
-        // number, so that what has been summed so far is scaled by a power of two, exactly.  Until then P <= 2^8,
-        // which bf16 and the fp32 sums hold.
-        uint32_t s[32];
-        tmem_ld32(s_addr, s);
-#pragma unroll 1
-        for (int c4 = 0; c4 < 4; ++c4) {
-          const float nm = m_used == -INFINITY ? 0.0f : -m_used;
+        // P = exp2(x - m) over S.  Mostly the exponentials use the running maximum m as it stands: P may grow to 2^20
+        // and the sums with it, which fp32 and bf16 hold without loss.  The first block of a run, one that some row does
+        // not see all of, and one where a row's sum passes that bound (rare; S is put back first) take the careful way:
+        // the maximum first, O and the sum moved to it where it grew by more than 2^8, then the exponentials.  It reads S
+        // in quarters from TMEM, in rolled loops: P of quarter c lies over quarter c / 2, so quarters in order never
+        // overwrite an unread one.
+        bool careful = j == 0 || cut;
+        float sum = 0.0f;
+        if (!careful) {
+          const float nm = -m_used;
           const uint64_t nm2 = pack2(nm, nm);
-          float xs[32], mq[4];
-          wait_ld_regs(s);
+          uint32_t sv[4][32];
+          tmem_ld32(s_addr, sv[0]);
+          tmem_ld32(s_addr + 32, sv[1]);
+          wait_ld_regs(sv[0]);
+          wait_ld_regs(sv[1]);
+          tmem_ld32(s_addr + 64, sv[2]);  // in flight while the first half's exponentials run
+          tmem_ld32(s_addr + 96, sv[3]);
+          uint64_t ls[2] = {0, 0};
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            uint64_t a2, b2, sp;
-            ld_shared_2x64(sc + (c4 * 16 + k) * 16, a2, b2);
-            asm("mov.b64 %0, {%1, %2};" : "=l"(sp) : "r"(s[2 * k]), "r"(s[2 * k + 1]));
-            unpack2(fma2(sp, a2, fma2(b2, qs2, nm2)), xs[2 * k], xs[2 * k + 1]);
+          for (int c4 = 0; c4 < 4; ++c4) {
+            if (c4 == 2) {
+              wait_ld_regs(sv[2]);
+              wait_ld_regs(sv[3]);
+            }
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint64_t a2[2];
+              ld_shared_2x64(sc + (c4 * 8 + k) * 16, a2[0], a2[1]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint64_t sp;
+                asm("mov.b64 %0, {%1, %2};" : "=l"(sp) : "r"(sv[c4][4 * k + 2 * e]), "r"(sv[c4][4 * k + 2 * e + 1]));
+                float x0, x1;
+                unpack2(fma2(sp, a2[e], nm2), x0, x1);
+                const float p0 = ex2(x0), p1 = ex2(x1);
+                ls[e] = add2(ls[e], pack2(p0, p1));
+                pk[2 * k + e] = pack_bf16x2(p0, p1);
+              }
+            }
+            tmem_st16(s_addr + c4 * 16, pk);
           }
-          if (c4 < 3) tmem_ld32(s_addr + (c4 + 1) * 32, s);
-          else if (kSepP) {  // S is in registers: the next one may come
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_free[x]);
+          float la, lb;
+          unpack2(add2(ls[0], ls[1]), la, lb);
+          sum = la + lb;
+          careful = __any_sync(0xffffffffu, sum > 1048576.0f || m_used == -INFINITY);
+          if (careful) {
+            tmem_st_wait();
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) tmem_st32(s_addr + c4 * 32, sv[c4]);
+            tmem_st_wait();
           }
-          if (cut) {
+        }
+        if (careful) {
+          uint32_t s[32];
+          auto scores = [&](int c4, float nm, float (&xs)[32]) {  // of quarter c4, relative to m; not seen: -infinity
+            tmem_ld32(s_addr + c4 * 32, s);
+            wait_ld_regs(s);
+            const uint64_t nm2 = pack2(nm, nm);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint64_t a2[2];
+              ld_shared_2x64(sc + (c4 * 8 + k) * 16, a2[0], a2[1]);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint64_t sp;
+                asm("mov.b64 %0, {%1, %2};" : "=l"(sp) : "r"(s[4 * k + 2 * e]), "r"(s[4 * k + 2 * e + 1]));
+                unpack2(fma2(sp, a2[e], nm2), xs[4 * k + 2 * e], xs[4 * k + 2 * e + 1]);
+              }
+            }
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               if (c4 * 32 + k >= left) xs[k] = -INFINITY;
+          };
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            float xs[32], mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            scores(c4, 0.0f, xs);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) mq[k & 3] = max3(mq[k & 3], xs[2 * k], xs[2 * k + 1]);
+            mx = fmaxf(mx, fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])));
           }
+          if (__any_sync(0xffffffffu, mx > m_used + 8.0f)) {
+            const float m_new = fmaxf(m_used, mx), f = m_new == -INFINITY ? 1.0f : ex2(m_used - m_new);
+            m_used = m_new;
+            l *= f;
+            if (j > 0) {  // before the first P V there is no O
+              uint32_t v[16];
+#pragma unroll 1
+              for (int cc = 0; cc < DH / 16; ++cc) {
+                tmem_ld16(o_addr + cc * 16, v);
+                tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mq[k] = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) mq[k & 3] = max3(mq[k & 3], xs[2 * k], xs[2 * k + 1]);
-          uint32_t pk[16];
-          uint64_t ls0, ls1;
-          auto exps = [&]() {
-            ls0 = ls1 = 0;
+                for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                tmem_st16(o_addr + cc * 16, v);
+              }
+            }
+          }
+          const float nm = m_used == -INFINITY ? 0.0f : -m_used;
+          sum = 0.0f;
+#pragma unroll 1
+          for (int c4 = 0; c4 < 4; ++c4) {
+            float xs[32];
+            scores(c4, nm, xs);
+            uint32_t pk[16];
+            uint64_t ls = 0;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const float p0 = ex2(xs[2 * k]), p1 = ex2(xs[2 * k + 1]);
-              if (k & 1) ls1 = add2(ls1, pack2(p0, p1));
-              else ls0 = add2(ls0, pack2(p0, p1));
+              ls = add2(ls, pack2(p0, p1));
               pk[k] = pack_bf16x2(p0, p1);
             }
-          };
-          exps();
-          if (kSepP && c4 == 0 && n_sig > 0) {  // P is rewritten, and O rescaled, only after the last P V
-            if (!(ok = mbar_wait(&pv_done[x], (n_sig - 1) & 1, ctl, 964))) break;
-            tc_fence_after();
+            float la, lb;
+            unpack2(ls, la, lb);
+            sum += la + lb;
+            tmem_st16(s_addr + c4 * 16, pk);
           }
-          const float mx = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-          if (__any_sync(0xffffffffu, mx > (m_used == -INFINITY ? -INFINITY : 8.0f))) {
-            float up = 0.0f, f = 1.0f;
-            if (m_used == -INFINITY) {  // first keys that the row sees: nothing has been summed
-              if (mx > -INFINITY) {
-                m_used = up = mx;
-                f = 0.0f;
-              }
-            } else if (mx > 8.0f) {
-              up = ceilf(mx);
-              m_used += up;
-              f = ex2(-up);
-            }
-            l *= f;
-            tmem_st_wait();
-            if (j > 0) {  // before the first P V there is no O
-#pragma unroll 1
-              for (int cc = 0; cc < DH / 16; ++cc) {
-                tmem_ld16(o_addr + cc * 16, pk);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) pk[k] = __float_as_uint(__uint_as_float(pk[k]) * f);
-                tmem_st16(o_addr + cc * 16, pk);
-              }
-            }
-#pragma unroll 1
-            for (int cc = 0; cc < c4; ++cc) {  // the block's earlier quarters of P
-              tmem_ld16(p_addr + cc * 16, pk);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) pk[k] = pack_bf16x2(bf_lo(pk[k]) * f, bf_hi(pk[k]) * f);
-              tmem_st16(p_addr + cc * 16, pk);
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k) xs[k] -= up;
-            exps();
-          }
-          float la, lb;
-          unpack2(add2(ls0, ls1), la, lb);
-          l += la + lb;
-          tmem_st16(p_addr + c4 * 16, pk);
         }
-        if (!ok) break;
+        l += sum;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[x]);
-        ++n_sig;
       }
       if (!ok) break;
       if (!(ok = mbar_wait(&rec_v[rec], v_ph, ctl, 965))) break;
@@ -712,7 +746,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
       }
       // no key seen: O = 0, LSE = -inf.  Scores that are NaN leave l = NaN, and stay NaN.
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      // 16 columns at a time through this warp's slab of shared memory, out in whole 32-byte sectors
+      // 16 columns at a time, each row's 32 bytes a whole sector
 #pragma unroll 1
       for (int cc = 0; cc < DH / 16; ++cc) {
         uint32_t ov[16];
@@ -736,21 +770,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
             }
           }
         }
-        __syncwarp();  // the slab's last rows have been read
         const float scale = poison ? NAN : inv;
+        if (at >= 0) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          st_shared_v4(stage + lane * 32 + ((k ^ ((lane >> 2) & 1)) << 4),
-                       pack_bf16x2(__uint_as_float(ov[8 * k]) * scale, __uint_as_float(ov[8 * k + 1]) * scale),
-                       pack_bf16x2(__uint_as_float(ov[8 * k + 2]) * scale, __uint_as_float(ov[8 * k + 3]) * scale),
-                       pack_bf16x2(__uint_as_float(ov[8 * k + 4]) * scale, __uint_as_float(ov[8 * k + 5]) * scale),
-                       pack_bf16x2(__uint_as_float(ov[8 * k + 6]) * scale, __uint_as_float(ov[8 * k + 7]) * scale));
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int row = 16 * k + (int)(lane >> 1), to = __shfl_sync(0xffffffffu, at, row);
-          const uint4 v = ld_shared_v4(stage + row * 32 + (((lane & 1) ^ ((row >> 2) & 1)) << 4));
-          if (to >= 0) st_global_v4(p.o + (size_t)to * DH + cc * 16 + (lane & 1) * 8, v.x, v.y, v.z, v.w);
+          for (int k = 0; k < 2; ++k)
+            st_global_v4(p.o + (size_t)at * DH + cc * 16 + k * 8,
+                         pack_bf16x2(__uint_as_float(ov[8 * k]) * scale, __uint_as_float(ov[8 * k + 1]) * scale),
+                         pack_bf16x2(__uint_as_float(ov[8 * k + 2]) * scale, __uint_as_float(ov[8 * k + 3]) * scale),
+                         pack_bf16x2(__uint_as_float(ov[8 * k + 4]) * scale, __uint_as_float(ov[8 * k + 5]) * scale),
+                         pack_bf16x2(__uint_as_float(ov[8 * k + 6]) * scale, __uint_as_float(ov[8 * k + 7]) * scale));
         }
       }
       tc_fence_before();
