@@ -10,7 +10,7 @@
 //     The product t_j sum(q_i) is one more contraction step of the tensor core: both factors in three bf16 parts (24
 //     bits), the six products that matter in six of its 16 columns.  So the softmax has one packed FMA for two scores,
 //     as one without codes would have, and scores are exact up to fp32 sums.  Applying the minimum in the softmax
-//     instead, a second packed FMA and twice the shared-memory reads, took 1016 us where this takes LONGUS (8 histories
+//     instead, a second packed FMA and twice the shared-memory reads, took 1016 us where this took 908 us (8 histories
 //     of 4096-8192 keys, 4 heads, 8192 rows each); rounding the keys to bf16 would put 2^-9 of every product into the
 //     scores.
 //   * V is rounded to bf16 once, as P is and as the output is: its error is a weighted mean of such roundings.
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         rec_step();
         if (keys == 0) continue;
         for (int x = 0; x < nx && ok; ++x) {
-          if (!(ok = mbar_wait(&q_empty[x], ph[x] ^ 1, ctl, 941))) break;
+          if (!(ok = mbar_wait_sleep<200>(&q_empty[x], ph[x] ^ 1, ctl, 941))) break;
           ph[x] ^= 1;
           ++n[x];
           mbar_arrive_expect_tx(&q_full[x], (uint32_t)tile_rows * DH * 2);
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
       const uint32_t staging = smem_u32(smem + L::off_staging);
       bool ok = true;
       for (bool more = true; more && ok; more = w.next(p)) {
-        if (!(ok = mbar_wait(&rec_empty[ri], rec_ph ^ 1, ctl, 952))) break;
+        if (!(ok = mbar_wait_sleep<200>(&rec_empty[ri], rec_ph ^ 1, ctl, 952))) break;
         const int n = w.count(), keys = w.q.L;
         if (lane == 0) {
           volatile Rec& r = recs[ri];
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
           return j < n && mine && key < keys ? table[key >> p.c.page_log2] : 0;
         };
         auto copy = [&](int kv, int j, int pg) -> bool {
-          if (!mbar_wait(&st_empty[si], sph ^ 1, ctl, 953)) return false;
+          if (!mbar_wait_sleep<200>(&st_empty[si], sph ^ 1, ctl, 953)) return false;
           const int key = (w.step + j) * BN + (int)lane * 16;
           const bool go = mine && key < keys;
           if (go && (unsigned)pg >= (unsigned)p.c.pages) {
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         }
         if (ok) ok = copy(1, n - 1, now);
       }
-      if (ok && mbar_wait(&rec_empty[ri], rec_ph ^ 1, ctl, 954) && lane == 0) {
+      if (ok && mbar_wait_sleep<200>(&rec_empty[ri], rec_ph ^ 1, ctl, 954) && lane == 0) {
         recs[ri].n = -1;
         mbar_arrive(&rec_full[ri]);
       }
@@ -429,14 +429,15 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         const bool v = i > 0 && ((i & 1) == 0 || i == 2 * n - 1);
         const int j = i == 2 * n - 1 ? n - 1 : v ? i / 2 - 1 : (i + 1) / 2;
         const int key0 = (step + j) * BN + 32 * dw, left = keys - key0;  // this warp's 32 keys, and how many there are
-        if (!(ok = mbar_wait(&st_full[si], sph, ctl, 957))) break;
+        if (!(ok = mbar_wait_sleep<100>(&st_full[si], sph, ctl, 957))) break;
         const uint32_t src = staging + si * L::kStaging;
         uint32_t sc;
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sc) : "r"(src + BN * (DH / 2) + (32 * dw + lane) * 4) : "memory");
         if ((int)lane >= left) sc = 0;  // places past the history: codes are always finite, a zero step makes zeros of V
-        if (!(ok = mbar_wait(&ring_empty[rs], rph ^ 1, ctl, 958))) break;
+        if (!(ok = mbar_wait_sleep<100>(&ring_empty[rs], rph ^ 1, ctl, 958))) break;
         const uint32_t slot = ring + rs * L::kTile + (part >> 1) * (BN * 128) + (32 * dw + sub) * 128;
         const uint32_t codes = src + (32 * dw + sub) * (DH / 2) + part * 16;
+        uint4 nx4 = ld_shared_v4(codes);
         if (!v) {
           // a and t of this lane's key.  A step of zero, or too small to count beside its minimum, is taken as a tiny one:
           // then t carries the minimum alone.
@@ -450,7 +451,8 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
                        t2 | t1 << 16, 0u);
 #pragma unroll 1
           for (int s = 0; s < ITER; ++s) {
-            const uint4 c = ld_shared_v4(codes + s * RPI * (DH / 2));
+            const uint4 c = nx4;
+            if (s + 1 < ITER) nx4 = ld_shared_v4(codes + (s + 1) * RPI * (DH / 2));
             const uint32_t cw[4] = {c.x, c.y, c.z, c.w}, sw = (RPI * s + sub) & 7;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -467,7 +469,8 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
           }
 #pragma unroll 1
           for (int s = 0; s < ITER; ++s) {
-            const uint4 c = ld_shared_v4(codes + s * RPI * (DH / 2));
+            const uint4 c = nx4;
+            if (s + 1 < ITER) nx4 = ld_shared_v4(codes + (s + 1) * RPI * (DH / 2));
             const uint32_t cw[4] = {c.x, c.y, c.z, c.w}, sw = (RPI * s + sub) & 7;
             const uint32_t rsc = __shfl_sync(0xffffffffu, sc, RPI * s + sub);
             const uint32_t st2 = __byte_perm(rsc, rsc, 0x1010), mn2 = __byte_perm(rsc, rsc, 0x3232);
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         if (i > 0) continue;
         // after a unit's first K block: sums of the query rows, the other factor of the extra contraction step
         for (int x = 0; x < nx && ok; ++x) {
-          if (!(ok = mbar_wait(&q_full[x], (qph >> x) & 1, ctl, 959))) break;
+          if (!(ok = mbar_wait_sleep<100>(&q_full[x], (qph >> x) & 1, ctl, 959))) break;
           qph ^= 1u << x;
           const uint32_t qrow = smem_u32(s_q) + x * L::kTile + trow * 128;
           float qs = 0.0f;

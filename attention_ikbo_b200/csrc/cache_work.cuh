@@ -143,6 +143,24 @@ __device__ __forceinline__ uint32_t value2(uint32_t c16, uint32_t step, uint32_t
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// mbar_wait that sleeps between polls.  A failed poll comes back after some 40 cycles and costs about ten instructions;
+// with a dozen waiting warps these were more than half of all instructions issued.
+template <int NS>
+__device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, const Ctl& ctl, int where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer();
+  for (uint32_t it = 1;; ++it) {
+    __nanosleep(NS);
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 0) {
+      if (ctl.aborted()) return false;
+      if (globaltimer() - t0 > ctl.limit_ns) {
+        ctl.fail(ROCS_ERR_TIMEOUT, where);
+        return false;
+      }
+    }
+  }
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
