@@ -2,12 +2,13 @@
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import NamedTuple
 
 import torch
 
 from . import _binding as _b
-from ._binding import NORMS, ROCS_BF16, ROCS_F32, RocsError, _check, _f32, _i32, _i64, _offsets, _on_tensor_device, _stream, _sz, _vp, _workspace
+from ._binding import NORMS, ROCS_BF16, ROCS_F32, RocsError, _f32, _i32, _i64, _offsets, _sz, _vp, _workspace
 
 _DTYPES = {torch.float32: ROCS_F32, torch.bfloat16: ROCS_BF16}
 
@@ -42,6 +43,15 @@ class DcaCacheArgs(ctypes.Structure):
                 ("workspace_bytes", _sz)]
 
 
+# The structures as packed bytes (native alignment): a call of a few microseconds on the device is not to wait for
+# ctypes to fill fields one by one.
+_SIDE = "PPPPPqqqq"
+_CACHE = "PPPPqqqq"
+_PACK_NORM = struct.Struct("@" + _SIDE + _SIDE + "qiifPqqiPN")
+_PACK_MOVE = struct.Struct("@" + _CACHE + "qqPPPPPPqqiPqqiPPN")
+_PACK_DCA = struct.Struct("@" + _CACHE + "qqqqfPPPPPPqPPPN")
+_NO_SIDE = (0,) * 9
+
 _ready = None
 
 
@@ -49,16 +59,13 @@ def _lib():
     global _ready
     if _ready is None or _ready is not _b._lib:
         lib = _b.load_library()
-        P = ctypes.POINTER
-        for name, argt in [("rocs_qk_norm_rope_workspace_size", [P(NormRopeArgs)]),
-                           ("rocs_cache_workspace_size", [P(CacheMoveArgs)]),
-                           ("rocs_dca_cache_workspace_size", [P(DcaCacheArgs)])]:
+        # argument structures are passed by address: a byref() of a Structure or packed bytes
+        for name in ("rocs_qk_norm_rope_workspace_size", "rocs_cache_workspace_size", "rocs_dca_cache_workspace_size"):
             getattr(lib, name).restype = _sz
-            getattr(lib, name).argtypes = argt
-        for name, argt in [("rocs_qk_norm_rope_forward", [P(NormRopeArgs), _vp]),
-                           ("rocs_rope_table", [_vp, _i64, _i64, ctypes.c_double, _vp]),
-                           ("rocs_cache_append", [P(CacheMoveArgs), _vp]), ("rocs_cache_read", [P(CacheMoveArgs), _vp]),
-                           ("rocs_dca_cache_forward", [P(DcaCacheArgs), _vp])]:
+            getattr(lib, name).argtypes = [_vp]
+        for name, argt in [("rocs_qk_norm_rope_forward", [_vp, _vp]), ("rocs_rope_table", [_vp, _i64, _i64, ctypes.c_double, _vp]),
+                           ("rocs_cache_append", [_vp, _vp]), ("rocs_cache_read", [_vp, _vp]),
+                           ("rocs_dca_cache_forward", [_vp, _vp])]:
             getattr(lib, name).restype = ctypes.c_int
             getattr(lib, name).argtypes = argt
         _ready = lib
@@ -92,43 +99,83 @@ def _hold(stream, *tensors):
                 t.record_stream(stream)
 
 
-def _cuda(t, dtype, what, dev, dims=None, contiguous=True):
+def _refuse(t, dtype, what, idx, dims, contiguous=True):
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and (dims is None or t.dim() == dims)):
         raise RocsError(1, f"{what} must be a {'' if dims is None else f'{dims}-dimensional '}CUDA tensor of {dtype}")
     if contiguous and not t.is_contiguous():
         raise RocsError(1, f"{what} must be contiguous")
-    if t.device != dev:
-        raise RocsError(1, f"{what} is on {t.device}, the call's tensors are on {dev}")
+    raise RocsError(1, f"{what} is on {t.device}, the call's tensors are on cuda:{idx}")
+
+
+def _ptr(t, dtype, what, idx, dims):
+    """Address of a contiguous tensor of device ``idx``."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != idx or t.dtype is not dtype or t.dim() != dims or not t.is_contiguous():
+        _refuse(t, dtype, what, idx, dims)
     return t.data_ptr()
 
 
-def _rows(t, dtype, what, dev, heads=None, dh=None):
-    """``t`` [n, heads, dh] whose tokens may lie apart: ``(pointer or None, row stride in elements)``."""
-    _cuda(t, dtype, what, dev, 3, contiguous=False)
-    if (heads is not None and t.shape[1] != heads) or (dh is not None and t.shape[2] != dh):
-        raise RocsError(1, f"{what} has heads and channels {tuple(t.shape[1:])}, expected {(heads, dh)}")
-    if t.numel() == 0:
-        return None, 0
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+def _rows(t, dtype, what, idx, heads=None, dh=None):
+    """``t`` [n, heads, dh] whose tokens may lie apart: ``(address or 0, row stride in elements)``."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != idx or t.dtype is not dtype or t.dim() != 3:
+        _refuse(t, dtype, what, idx, 3, False)
+    n, h, d = t.shape
+    if (heads is not None and h != heads) or (dh is not None and d != dh):
+        raise RocsError(1, f"{what} has heads and channels {(h, d)}, expected {(heads, dh)}")
+    row = h * d
+    if n * row == 0:
+        return 0, 0
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    st = t.stride()
+    if st[2] != 1 or (h > 1 and st[1] != d):
         raise RocsError(1, f"{what}: the heads of a token must be dense (only tokens may lie apart)")
-    row = t.shape[1] * t.shape[2]
-    ld = t.stride(0) if t.shape[0] > 1 else row
+    ld = st[0] if n > 1 else row
     if ld < row:
         raise RocsError(1, f"{what}: tokens overlap (stride {ld}, {row} values a token)")
     return t.data_ptr(), ld
 
 
-def _rope(rope, dev):
-    """(pointer, positions, rotated channels) of a rope table, or of none."""
+def _rope(rope, idx):
+    """(address, positions, rotated channels) of a rope table, or of none."""
     if rope is None:
-        return None, 0, 0
-    return _cuda(rope, torch.float32, "rope", dev, 2), rope.shape[0], rope.shape[1]
+        return 0, 0, 0
+    return (_ptr(rope, torch.float32, "rope", idx, 2), *rope.shape)
 
 
-@_on_tensor_device
-def _fill_rope(table, base, stream):
-    _check(_lib().rocs_rope_table(table.data_ptr() if table.numel() else None, table.shape[0], table.shape[1], float(base),
-                                  _stream(stream)), "rocs_rope_table")
+def _csr(off, dev, idx, what):
+    """(device tensor, host array, device address, host address, R, total) of CSR offsets."""
+    d, h = _offsets(off, dev)
+    R = len(h) - 1
+    if R < 0 or h.dtype != "int32" or not h.flags.c_contiguous:
+        raise RocsError(1, f"{what}: host offsets must be a dense int32 array of R + 1 entries")
+    ptr = _ptr(d, torch.int32, what, idx, 1)
+    if d.shape[0] != R + 1:
+        raise RocsError(1, f"{what}: {d.shape[0]} offsets on the device, {R + 1} on the host")
+    return d, h, ptr, h.__array_interface__["data"][0], R, int(h[R])
+
+
+def _on(t, what, fn, args, dims=None):
+    """``fn(index of t's device, *args)`` with that device current."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise RocsError(1, f"{what} must be a CUDA tensor")
+    idx = t.get_device()
+    if idx == torch.cuda.current_device():
+        return fn(idx, *args)
+    with torch.cuda.device(idx):
+        return fn(idx, *args)
+
+
+def _run(fn, packed, stream, idx, what):
+    rc = fn(packed, torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
+    if rc != 0:
+        raise RocsError(rc, what)
+
+
+def _fill_rope(idx, table, base, stream):
+    rc = _lib().rocs_rope_table(table.data_ptr() if table.numel() else None, table.shape[0], table.shape[1], float(base),
+                                torch._C._cuda_getCurrentRawStream(idx) if stream is None else stream.cuda_stream)
+    if rc != 0:
+        raise RocsError(rc, "rocs_rope_table")
 
 
 def rocs_rope_table(max_pos, rot, base=10000.0, device="cuda", stream=None):
@@ -137,35 +184,41 @@ def rocs_rope_table(max_pos, rot, base=10000.0, device="cuda", stream=None):
     if max_pos < 0 or rot <= 0:
         raise RocsError(1, "rocs_rope_table: max_pos >= 0 and rot > 0")
     table = torch.empty((int(max_pos), int(rot)), dtype=torch.float32, device=device)
-    _fill_rope(table, base, stream)
+    _on(table, "device", _fill_rope, (table, base, stream))
+    _hold(stream, table)
     return table
 
 
-def _side(x, out, pos, gamma, beta, rope, what, dev, dtype, dh):
+def _side(x, out, pos, gamma, beta, rope, what, idx, dtype, dh):
     if x is None:
-        return NormRopeSide(), None
-    x_ptr, ld_x = _rows(x, dtype, what, dev, None, dh)
+        return _NO_SIDE, None
+    x_ptr, ld_x = _rows(x, dtype, what, idx, None, dh)
     if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=dev)
-    elif tuple(out.shape) != tuple(x.shape):
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=dtype, device=x.device)
+    elif out.shape != x.shape:
         raise RocsError(1, f"{what}_out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
-    out_ptr, ld_out = _rows(out, dtype, what + "_out", dev)
-    n = x.shape[0] if x.numel() else 0
+    out_ptr, ld_out = _rows(out, dtype, what + "_out", idx)
+    n, heads, _ = x.shape
+    p_ptr = g_ptr = b_ptr = 0
     if rope is not None:
         if pos is None:
             raise RocsError(1, f"pos_{what} must be given with a rope table")
-        if pos.dim() != 1 or pos.shape[0] != x.shape[0]:
+        p_ptr = _ptr(pos, torch.int32, "pos_" + what, idx, 1)
+        if pos.shape[0] != n:
             raise RocsError(1, f"pos_{what} must have one position for each token")
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        if t is not None and tuple(t.shape) != (dh,):
-            raise RocsError(1, f"{name}_{what} must have {dh} values")
-    return NormRopeSide(x=x_ptr, out=out_ptr, pos=None if rope is None else _cuda(pos, torch.int32, "pos_" + what, dev),
-                        gamma=None if gamma is None else _cuda(gamma, torch.float32, "gamma_" + what, dev),
-                        beta=None if beta is None else _cuda(beta, torch.float32, "beta_" + what, dev),
-                        n=n, heads=x.shape[1] if n else 0, ld_x=ld_x, ld_out=ld_out), out
+    if gamma is not None:
+        g_ptr = _ptr(gamma, torch.float32, "gamma_" + what, idx, 1)
+        if gamma.shape[0] != dh:
+            raise RocsError(1, f"gamma_{what} must have {dh} values")
+    if beta is not None:
+        b_ptr = _ptr(beta, torch.float32, "beta_" + what, idx, 1)
+        if beta.shape[0] != dh:
+            raise RocsError(1, f"beta_{what} must have {dh} values")
+    if x_ptr == 0:
+        return _NO_SIDE, out
+    return (x_ptr, out_ptr, p_ptr, g_ptr, b_ptr, n, heads, ld_x, ld_out), out
 
 
-@_on_tensor_device
 def rocs_qk_norm_rope_forward(q, k=None, pos_q=None, pos_k=None, rope=None, norm="rmsnorm", gamma_q=None, gamma_k=None,
                               beta_q=None, beta_k=None, eps=1e-6, interleaved=False, q_out=None, k_out=None,
                               workspace=None, stream=None):
@@ -173,70 +226,72 @@ def rocs_qk_norm_rope_forward(q, k=None, pos_q=None, pos_k=None, rope=None, norm
     the tokens' positions in one pass.  ``rope``: the table of :func:`rocs_rope_table`, or None for no rotation.
     ``norm``: "none", "layernorm" or "rmsnorm".  Tokens may lie apart (rows of a wider projection output); an output
     may be its own input.  Returns ``(q_out, k_out)``."""
-    lib = _lib()
     x = q if q is not None else k
     if x is None:
         raise RocsError(1, "rocs_qk_norm_rope_forward: q or k must be given")
-    if x.dtype not in _DTYPES or x.dim() != 3:
+    return _on(x, "q" if q is not None else "k", _norm_rope,
+               (x, q, k, pos_q, pos_k, rope, norm, gamma_q, gamma_k, beta_q, beta_k, eps, interleaved, q_out, k_out, workspace, stream))
+
+
+def _norm_rope(idx, x, q, k, pos_q, pos_k, rope, norm, gamma_q, gamma_k, beta_q, beta_k, eps, interleaved, q_out, k_out, workspace,
+               stream):
+    dtype = x.dtype
+    if dtype not in _DTYPES or x.dim() != 3:
         raise RocsError(1, "q and k must be [tokens, heads, dh] of bf16 or fp32")
-    dev, dtype, dh = x.device, x.dtype, x.shape[2]
-    sq, q_out = _side(q, q_out, pos_q, gamma_q, beta_q, rope, "q", dev, dtype, dh)
-    sk, k_out = _side(k, k_out, pos_k, gamma_k, beta_k, rope, "k", dev, dtype, dh)
-    rp, max_pos, rot = _rope(rope, dev)
-    ws = _workspace(256, dev, workspace)
-    a = NormRopeArgs(q=sq, k=sk, dh=dh, dtype=_DTYPES[dtype], norm=NORMS[norm] if isinstance(norm, str) else int(norm),
-                     eps=float(eps), rope=rp, max_pos=max_pos, rot=rot, interleaved=int(bool(interleaved)),
-                     workspace=ws.data_ptr(), workspace_bytes=ws.numel() * ws.element_size())
-    _check(lib.rocs_qk_norm_rope_forward(ctypes.byref(a), _stream(stream)), "rocs_qk_norm_rope_forward")
+    dh = x.shape[2]
+    sq, q_out = _side(q, q_out, pos_q, gamma_q, beta_q, rope, "q", idx, dtype, dh)
+    sk, k_out = _side(k, k_out, pos_k, gamma_k, beta_k, rope, "k", idx, dtype, dh)
+    ws = _workspace(256, x.device, workspace)
+    _run(_lib().rocs_qk_norm_rope_forward,
+         _PACK_NORM.pack(*sq, *sk, dh, _DTYPES[dtype], NORMS[norm] if isinstance(norm, str) else int(norm), eps, *_rope(rope, idx),
+                         1 if interleaved else 0, ws.data_ptr(), ws.nbytes), stream, idx, "rocs_qk_norm_rope_forward")
     _hold(stream, ws, q_out, k_out)
     rocs_qk_norm_rope_forward.last_workspace = ws
     return q_out, k_out
 
 
-def _cache(cache, dev):
-    kc = cache.k_codes
-    _cuda(kc, torch.uint8, "cache.k_codes", dev, 4)
+def _cache(cache, idx):
+    kc, vc, ks, vs = cache.k_codes, cache.v_codes, cache.k_scale, cache.v_scale
+    ptrs = (_ptr(kc, torch.uint8, "cache.k_codes", idx, 4), _ptr(vc, torch.uint8, "cache.v_codes", idx, 4),
+            _ptr(ks, torch.bfloat16, "cache.k_scale", idx, 4), _ptr(vs, torch.bfloat16, "cache.v_scale", idx, 4))
     pages, heads, page, half = kc.shape
-    for name, t, dtype, shape in (("v_codes", cache.v_codes, torch.uint8, (pages, heads, page, half)),
-                                  ("k_scale", cache.k_scale, torch.bfloat16, (pages, heads, page, 2)),
-                                  ("v_scale", cache.v_scale, torch.bfloat16, (pages, heads, page, 2))):
-        _cuda(t, dtype, "cache." + name, dev)
-        if tuple(t.shape) != shape:
-            raise RocsError(1, f"cache.{name} has shape {tuple(t.shape)}, expected {shape}")
-    return CacheQ4Args(k_codes=kc.data_ptr(), v_codes=cache.v_codes.data_ptr(), k_scale=cache.k_scale.data_ptr(),
-                       v_scale=cache.v_scale.data_ptr(), pages=pages, page=page, heads=heads, dh=2 * half)
+    if vc.shape != kc.shape or ks.shape != vs.shape or ks.shape != (pages, heads, page, 2):
+        raise RocsError(1, f"cache: codes {tuple(kc.shape)}, {tuple(vc.shape)}, scale {tuple(ks.shape)}, {tuple(vs.shape)} do not belong "
+                           "together")
+    return ptrs + (pages, page, heads, 2 * half)
 
 
-def _table(page_table, R, dev):
-    ptr = _cuda(page_table, torch.int32, "page_table", dev, 2)
-    if page_table.shape[0] != R:
-        raise RocsError(1, f"page_table has {page_table.shape[0]} rows for {R} requests")
-    return ptr if page_table.numel() else None
+def _table(page_table, R, idx):
+    """(address, pages of a row)"""
+    ptr = _ptr(page_table, torch.int32, "page_table", idx, 2)
+    rows, cols = page_table.shape
+    if rows != R:
+        raise RocsError(1, f"page_table has {rows} rows for {R} requests")
+    return ptr, cols
 
 
-def _per_request(t, R, what, dev):
-    ptr = _cuda(t, torch.int32, what, dev, 1)
+def _per_request(t, R, what, idx):
+    ptr = _ptr(t, torch.int32, what, idx, 1)
     if t.shape[0] != R:
         raise RocsError(1, f"{what} has {t.shape[0]} entries for {R} requests")
-    return ptr if R else None
+    return ptr
 
 
-def _move(cache, k, v, tok_off, base, page_table, dtype, dev, workspace):
-    off_d, off_h = _offsets(tok_off, dev)
-    R, T = len(off_h) - 1, int(off_h[-1])
-    _cuda(off_d, torch.int32, "tok_off", dev, 1)
-    c = _cache(cache, dev)
-    for t, n in ((k, "k"), (v, "v")):
-        if t.shape[0] != T:
-            raise RocsError(1, f"{n} has {t.shape[0]} tokens, tok_off counts {T}")
-    k_ptr, k_ld = _rows(k, dtype, "k", dev, c.heads, c.dh)
-    v_ptr, v_ld = _rows(v, dtype, "v", dev, c.heads, c.dh)
-    ws = _workspace(256, dev, workspace)
-    return CacheMoveArgs(cache=c, R=R, max_pages=page_table.shape[1], tok_off_dev=off_d.data_ptr(),
-                         tok_off_host=off_h.ctypes.data, base=_per_request(base, R, "base", dev),
-                         page_table=_table(page_table, R, dev), k=k_ptr, v=v_ptr, k_ld=k_ld, v_ld=v_ld,
-                         dtype=_DTYPES[dtype], workspace=ws.data_ptr(),
-                         workspace_bytes=ws.numel() * ws.element_size()), (off_d, off_h), ws
+def _move(fn, what, idx, c, csr, k, v, base, page_table, rope, pos, interleaved, dtype, ws, stream):
+    _, _, off_d, off_h, R, T = csr
+    k_ptr, k_ld = _rows(k, dtype, "k", idx, c[6], c[7])
+    v_ptr, v_ld = _rows(v, dtype, "v", idx, c[6], c[7])
+    if k.shape[0] != T or v.shape[0] != T:
+        raise RocsError(1, f"k and v have {k.shape[0]} and {v.shape[0]} tokens, tok_off counts {T}")
+    table, cols = _table(page_table, R, idx)
+    p_ptr = 0
+    if pos is not None:
+        p_ptr = _ptr(pos, torch.int32, "pos", idx, 1)
+        if pos.shape[0] != T:
+            raise RocsError(1, "pos must have one position for each token")
+    _run(fn, _PACK_MOVE.pack(*c, R, cols, off_d, off_h, _per_request(base, R, "base", idx), table, k_ptr, v_ptr, k_ld, v_ld,
+                             _DTYPES[dtype], *_rope(rope, idx), 1 if interleaved else 0, p_ptr, ws.data_ptr(), ws.nbytes),
+         stream, idx, what)
 
 
 def rocs_cache_append(cache, k, v, tok_off, base, page_table, rope=None, pos=None, interleaved=False, workspace=None,
@@ -244,24 +299,17 @@ def rocs_cache_append(cache, k, v, tok_off, base, page_table, rope=None, pos=Non
     """Append ``k``, ``v`` [T, heads, dh] (bf16 or fp32) to the histories of a :class:`CacheQ4`: token ``i`` of request
     ``r`` (row ``tok_off[r] + i``) goes to slot ``base[r] + i``, keys rotated by ``pos`` (default: the slot) on the way.
     ``base`` [R] int32 is not changed.  Returns ``cache``."""
-    return _append(k, cache, v, tok_off, base, page_table, rope, pos, interleaved, workspace, stream)
+    return _on(k, "k", _append, (cache, k, v, tok_off, base, page_table, rope, pos, interleaved, workspace, stream))
 
 
-@_on_tensor_device
-def _append(k, cache, v, tok_off, base, page_table, rope, pos, interleaved, workspace, stream):
-    lib = _lib()
+def _append(idx, cache, k, v, tok_off, base, page_table, rope, pos, interleaved, workspace, stream):
     if k.dtype not in _DTYPES:
         raise RocsError(1, "k and v must be bf16 or fp32")
-    dev = k.device
-    a, keep, ws = _move(cache, k, v, tok_off, base, page_table, k.dtype, dev, workspace)
-    a.rope, a.max_pos, a.rot = _rope(rope, dev)
-    a.interleaved = int(bool(interleaved))
-    if pos is not None:
-        if pos.dim() != 1 or pos.shape[0] != k.shape[0]:
-            raise RocsError(1, "pos must have one position for each token")
-        a.pos = _cuda(pos, torch.int32, "pos", dev) if pos.numel() else None
-    _check(lib.rocs_cache_append(ctypes.byref(a), _stream(stream)), "rocs_cache_append")
-    _hold(stream, ws, keep[0])
+    csr = _csr(tok_off, k.device, idx, "tok_off")
+    ws = _workspace(256, k.device, workspace)
+    _move(_lib().rocs_cache_append, "rocs_cache_append", idx, _cache(cache, idx), csr, k, v, base, page_table, rope, pos, interleaved,
+          k.dtype, ws, stream)
+    _hold(stream, ws, csr[0])
     rocs_cache_append.last_workspace = ws
     return cache
 
@@ -269,64 +317,63 @@ def _append(k, cache, v, tok_off, base, page_table, rope, pos, interleaved, work
 def rocs_cache_read(cache, tok_off, base, page_table, k=None, v=None, workspace=None, stream=None):
     """Slots ``base[r] ... base[r] + tok_off[r+1] - tok_off[r] - 1`` of every request's history as bf16 values, dense:
     ``(k, v)`` [T, heads, dh], what :func:`rocs_dca_forward` reads."""
-    return _read(cache.k_codes, cache, tok_off, base, page_table, k, v, workspace, stream)
+    return _on(cache.k_codes, "cache.k_codes", _read, (cache, tok_off, base, page_table, k, v, workspace, stream))
 
 
-@_on_tensor_device
-def _read(k_codes, cache, tok_off, base, page_table, k, v, workspace, stream):
-    lib = _lib()
-    dev = k_codes.device
-    off = _offsets(tok_off, dev)
-    shape = (int(off[1][-1]), k_codes.shape[1], 2 * k_codes.shape[3])
-    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-    a, keep, ws = _move(cache, k, v, off, base, page_table, torch.bfloat16, dev, workspace)
-    _check(lib.rocs_cache_read(ctypes.byref(a), _stream(stream)), "rocs_cache_read")
-    _hold(stream, ws, keep[0], k, v)
+def _read(idx, cache, tok_off, base, page_table, k, v, workspace, stream):
+    dev = cache.k_codes.device
+    csr = _csr(tok_off, dev, idx, "tok_off")
+    c = _cache(cache, idx)
+    if k is None:
+        k = torch.empty((csr[5], c[6], c[7]), dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty_like(k) if k.is_contiguous() else torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
+    ws = _workspace(256, dev, workspace)
+    _move(_lib().rocs_cache_read, "rocs_cache_read", idx, c, csr, k, v, base, page_table, None, None, False, torch.bfloat16, ws, stream)
+    _hold(stream, ws, csr[0], k, v)
     rocs_cache_read.last_workspace = ws
     return k, v
 
 
-@_on_tensor_device
 def rocs_dca_cache_forward(q_t, cache, page_table, seq_len, cand_off, q_tokens, scale, key_limit=None, o=None, lse=True,
                            workspace=None, stream=None):
     """IKBO-DCA over a :class:`CacheQ4`: ``q_t`` [C*q, H, dh] bf16 (tokens may lie apart, H a multiple of the cache's
     heads), ``seq_len`` [R] int32 keys of each history, ``key_limit`` [C] int32 (optional) keys that a candidate sees.
     Returns ``(o [C*q, H, dh], lse [C*q, H] or None)``."""
+    return _on(q_t, "q", _dca_cache, (q_t, cache, page_table, seq_len, cand_off, q_tokens, scale, key_limit, o, lse, workspace, stream))
+
+
+def _dca_cache(idx, q_t, cache, page_table, seq_len, cand_off, q_tokens, scale, key_limit, o, lse, workspace, stream):
     lib = _lib()
-    dev = q_t.device
-    off_d, off_h = _offsets(cand_off, dev)
-    R, C = len(off_h) - 1, int(off_h[-1])
-    _cuda(off_d, torch.int32, "cand_off", dev, 1)
-    c = _cache(cache, dev)
-    q_ptr, q_ld = _rows(q_t, torch.bfloat16, "q", dev, None, c.dh)
-    if q_t.shape[0] != C * q_tokens:
-        raise RocsError(1, f"q has {q_t.shape[0]} tokens, cand_off counts {C} candidates of {q_tokens}")
-    shape = tuple(q_t.shape)
+    off_dev, _, off_d, off_h, R, C = _csr(cand_off, q_t.device, idx, "cand_off")
+    c = _cache(cache, idx)
+    q_ptr, q_ld = _rows(q_t, torch.bfloat16, "q", idx, None, c[7])
+    n, H, dh = q_t.shape
+    if n != C * q_tokens:
+        raise RocsError(1, f"q has {n} tokens, cand_off counts {C} candidates of {q_tokens}")
     if o is None:
-        o = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _cuda(o, torch.bfloat16, "o", dev)
+        o = torch.empty_like(q_t) if q_t.is_contiguous() else torch.empty((n, H, dh), dtype=torch.bfloat16, device=q_t.device)
+    elif o.shape != q_t.shape:
+        raise RocsError(1, f"o has shape {tuple(o.shape)}, expected {(n, H, dh)}")
     if lse is True:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=dev)
+        lse = torch.empty((n, H), dtype=torch.float32, device=q_t.device)
     elif lse is False:
         lse = None
-    for t, want, what in ((o, shape, "o"), (lse, shape[:2], "lse")):
-        if t is not None and tuple(t.shape) != want:
-            raise RocsError(1, f"{what} has shape {tuple(t.shape)}, expected {want}")
-    if key_limit is not None and tuple(key_limit.shape) != (C,):
-        raise RocsError(1, f"key_limit must have one entry for each of {C} candidates")
-    a = DcaCacheArgs(cache=c, R=R, q=int(q_tokens), H=shape[1], max_pages=page_table.shape[1], scale=float(scale),
-                     cand_off_dev=off_d.data_ptr(), cand_off_host=off_h.ctypes.data,
-                     seq_len=_per_request(seq_len, R, "seq_len", dev), page_table=_table(page_table, R, dev),
-                     key_limit=None if key_limit is None or C == 0 else _cuda(key_limit, torch.int32, "key_limit", dev),
-                     q_ptr=q_ptr, q_ld=q_ld, o_ptr=o.data_ptr() if C else None,
-                     lse_ptr=_cuda(lse, torch.float32, "lse", dev) if lse is not None and C else None)
-    nbytes = lib.rocs_dca_cache_workspace_size(ctypes.byref(a))
-    if nbytes == 0:
-        _check(lib.rocs_dca_cache_forward(ctypes.byref(a), _stream(stream)), "rocs_dca_cache_forward")
-    ws = _workspace(nbytes, dev, workspace)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    _check(lib.rocs_dca_cache_forward(ctypes.byref(a), _stream(stream)), "rocs_dca_cache_forward")
-    _hold(stream, ws, off_d, o, lse)
+    lse_ptr = lim_ptr = 0
+    if lse is not None:
+        lse_ptr = _ptr(lse, torch.float32, "lse", idx, 2)
+        if lse.shape != (n, H):
+            raise RocsError(1, f"lse has shape {tuple(lse.shape)}, expected {(n, H)}")
+    if key_limit is not None:
+        lim_ptr = _ptr(key_limit, torch.int32, "key_limit", idx, 1)
+        if key_limit.shape[0] != C:
+            raise RocsError(1, f"key_limit must have one entry for each of {C} candidates")
+    table, cols = _table(page_table, R, idx)
+    a = (*c, R, int(q_tokens), H, cols, scale, off_d, off_h, _per_request(seq_len, R, "seq_len", idx), table, lim_ptr, q_ptr, q_ld,
+         _ptr(o, torch.bfloat16, "o", idx, 3), lse_ptr)
+    nbytes = lib.rocs_dca_cache_workspace_size(_PACK_DCA.pack(*a, 0, 0))
+    ws = _workspace(nbytes, q_t.device, workspace)  # 0: refused arguments, the call below says which
+    _run(lib.rocs_dca_cache_forward, _PACK_DCA.pack(*a, ws.data_ptr(), ws.nbytes), stream, idx, "rocs_dca_cache_forward")
+    _hold(stream, ws, off_dev, o, lse)
     rocs_dca_cache_forward.last_workspace = ws
     return o, lse

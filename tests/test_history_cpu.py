@@ -147,6 +147,26 @@ def test_cache_attention_refusals(lib):
     assert size(P(args(off=(0, 0), q_ptr=None, o_ptr=None, seq_len=None, page_table=None))) == 256
 
 
+def test_packed_arguments_match_the_structures():
+    import attention_ikbo_b200._history as m
+
+    for pack, args in ((m._PACK_NORM, m.NormRopeArgs), (m._PACK_MOVE, m.CacheMoveArgs), (m._PACK_DCA, m.DcaCacheArgs)):
+        assert pack.size == ctypes.sizeof(args)
+        # every field at its place: distinct numbers through both forms
+        flat = []
+
+        def walk(t, at):
+            for name, kind in t._fields_:
+                off = at + getattr(t, name).offset
+                if issubclass(kind, ctypes.Structure):
+                    walk(kind, off)
+                else:
+                    flat.append((off, kind))
+        walk(args, 0)
+        data = bytearray(pack.pack(*range(1, len(flat) + 1)))
+        assert [kind.from_buffer(data, off).value for off, kind in flat] == list(range(1, len(flat) + 1))
+
+
 def test_binding_refuses_host_tensors():
     import attention_ikbo_b200 as m
 
