@@ -14,7 +14,7 @@ struct NormRopeSide {
   const float* gamma;  // [dh] or null
   const float* beta;   // [dh] or null
   int64_t ld_x, ld_out;
-  int n, heads, groups;  // groups: warps per token
+  int n, heads;
 };
 struct NormRopeParams {
   NormRopeSide side[2];  // queries, keys
@@ -25,12 +25,11 @@ struct NormRopeParams {
   WsHeader* ws;
 };
 cudaError_t launch_norm_rope(const NormRopeParams& p, int dh, bool f32, int unroll, cudaStream_t st);
-// rows of one head that a warp of the kernels below handles at a time, and how many such steps are unrolled
-inline int rows_per_warp(int64_t dh) { return (int)(256 / dh); }
-inline int unroll_for(int64_t heads, int64_t dh) {
-  const int64_t steps = (heads + rows_per_warp(dh) - 1) / rows_per_warp(dh);
-  return steps >= 4 ? 4 : steps >= 2 ? 2 : 1;
-}
+// rows that a warp of the kernels below holds at a time; with few of them (less than the device's warps) a warp takes one
+// such set, so that as many SMs as possible work on a small call, otherwise several, so that more loads are in flight
+inline int rows_per_warp(int64_t dh) { return (int)(512 / dh); }
+inline int unroll_for(int64_t rows, int64_t dh, int sms, int most) { return rows >= (int64_t)sms * 32 * rows_per_warp(dh) ? most : 1; }
+constexpr int kNormSets = 2, kAppendSets = 2, kReadSets = 4;
 cudaError_t launch_rope_table(float* table, int64_t max_pos, int rot, double base, cudaStream_t st);
 
 // ---------------------------------------------------------------- the paged 4-bit cache
@@ -49,8 +48,8 @@ struct CacheMoveParams {  // append and read
   const int32_t* table;    // [R, max_pages]
   const int32_t* pos;      // [T] or null
   const float* rope;
-  int R, max_pages, max_pos, rot, interleaved, groups;
-  int64_t warps;           // T * 2 * groups
+  int R, max_pages, max_pos, rot, interleaved;
+  int64_t rows, warps;     // T * heads; warps for one of keys and values
   WsHeader* ws;
 };
 cudaError_t launch_cache_append(const CacheMoveParams& p, int dh, bool f32, int unroll, cudaStream_t st);

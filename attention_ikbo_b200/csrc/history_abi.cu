@@ -43,7 +43,7 @@ int side_validate(const rocs_norm_rope_side& s, const rocs_norm_rope_args* a) {
   if (s.n == 0) return ROCS_OK;
   if (s.heads == 0 || !s.x || !s.out) return ROCS_ERR_INVALID_ARG;
   const int64_t row = s.heads * a->dh, es = a->dtype == ROCS_BF16 ? 2 : 4;
-  if (s.n >= (int64_t(1) << 31) || row >= (int64_t(1) << 24)) return ROCS_ERR_UNSUPPORTED;
+  if (s.n >= (int64_t(1) << 31) || row >= (int64_t(1) << 24) || s.n * s.heads >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
   const int64_t ldx = s.ld_x ? s.ld_x : row, ldo = s.ld_out ? s.ld_out : row;
   if (ldx < row || ldo < row) return ROCS_ERR_INVALID_ARG;
   if ((ldx * es) % 16 || (ldo * es) % 16 || ldx >= (int64_t(1) << 31) || ldo >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
@@ -127,6 +127,7 @@ int move_validate(const rocs_cache_move_args* a, bool append, int64_t* T) {
   if (*T == 0) return ROCS_OK;
   if (!a->tok_off_dev || !a->base || !a->k || !a->v || (a->max_pages > 0 && !a->page_table)) return ROCS_ERR_INVALID_ARG;
   if (!al(a->k, 16) || !al(a->v, 16) || !al(a->base, 4) || !al(a->page_table, 4) || !al(a->pos, 4)) return ROCS_ERR_INVALID_ARG;
+  if (*T * a->cache.heads >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
   const int64_t row = a->cache.heads * a->cache.dh, es = a->dtype == ROCS_BF16 ? 2 : 4;
   for (int64_t ld : {a->k_ld, a->v_ld}) {
     if (ld != 0 && ld < row) return ROCS_ERR_INVALID_ARG;
@@ -158,10 +159,10 @@ int cache_move(const rocs_cache_move_args* a, bool append, cudaStream_t st) {
   p.rot = (int)a->rot;
   p.interleaved = a->interleaved != 0;
   p.ws = static_cast<WsHeader*>(a->workspace);
-  const int unroll = unroll_for(a->cache.heads, a->cache.dh), per = unroll * rows_per_warp(a->cache.dh);
-  p.groups = (int)((a->cache.heads + per - 1) / per);
-  p.warps = T * 2 * p.groups;
-  if (p.warps >= (int64_t(1) << 33)) return ROCS_ERR_UNSUPPORTED;
+  p.rows = T * a->cache.heads;
+  const int unroll = unroll_for(p.rows, a->cache.dh, sm_count_ext(), append ? kAppendSets : kReadSets);
+  const int per = unroll * rows_per_warp(a->cache.dh);
+  p.warps = (p.rows + per - 1) / per;
   if (cudaMemsetAsync(p.ws, 0, sizeof(WsHeader), st) != cudaSuccess) return ROCS_ERR_CUDA;
   if (T > 0) {
     const cudaError_t e = append ? launch_cache_append(p, (int)a->cache.dh, a->dtype == ROCS_F32, unroll, st)
@@ -297,8 +298,8 @@ int rocs_qk_norm_rope_forward(const rocs_norm_rope_args* a, rocs_stream_t stream
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   NormRopeParams p;
   std::memset(&p, 0, sizeof(p));
-  const int64_t heads = a->q.n == 0 ? a->k.heads : a->k.n == 0 ? a->q.heads : a->q.heads > a->k.heads ? a->q.heads : a->k.heads;
-  const int unroll = unroll_for(heads, a->dh), per = unroll * rows_per_warp(a->dh);
+  const int64_t rows[2] = {a->q.n * a->q.heads, a->k.n * a->k.heads};
+  const int unroll = unroll_for(rows[0] + rows[1], a->dh, sm_count_ext(), kNormSets), per = unroll * rows_per_warp(a->dh);
   const rocs_norm_rope_side* s[2] = {&a->q, &a->k};
   for (int i = 0; i < 2; ++i) {
     const int64_t row = s[i]->heads * a->dh;
@@ -311,11 +312,9 @@ int rocs_qk_norm_rope_forward(const rocs_norm_rope_args* a, rocs_stream_t stream
     p.side[i].ld_out = s[i]->ld_out ? s[i]->ld_out : row;
     p.side[i].n = (int)s[i]->n;
     p.side[i].heads = (int)s[i]->heads;
-    p.side[i].groups = (int)((s[i]->heads + per - 1) / per);
-    p.warps += s[i]->n * p.side[i].groups;
+    p.warps += (rows[i] + per - 1) / per;
     if (i == 0) p.warps0 = p.warps;
   }
-  if (p.warps >= (int64_t(1) << 33)) return ROCS_ERR_UNSUPPORTED;
   p.rope = a->rope;
   p.max_pos = (int)a->max_pos;
   p.rot = (int)a->rot;

@@ -5,9 +5,11 @@
 //   y = (x - mean) / sqrt(var + eps) * gamma + beta       (Layer; population variance, two passes over registers)
 //   (a, b) -> (a c - b s, b c + a s)                      for each of the rot/2 pairs of channels, angle of the token
 //
-// One pass: each value is read and written once, so memory bounds it.  A warp takes one token and up to four steps of
-// 256/dh heads: its part of the table row and of gamma and beta stay in registers for all of them, and the loads of
-// all steps are in flight before the first is used.  Statistics and rotation in fp32, one rounding when stored.
+// One pass: each value is read and written once, so memory bounds it.  A warp takes U * 512/dh rows (heads of tokens, in
+// their order); the loads of all of them are in flight before the first is used, and values stay packed as they came
+// until their row's turn, so that enough warps fit an SM.  Statistics and rotation in fp32, one rounding when stored.
+// With 8 channels to a lane (half the rows to a warp, partners of a pair 8 lanes apart, one token to a warp) it took 131 us
+// where this takes NRUS (16384 x 8 query and 65536 x 8 key rows of 128, bf16).
 #include "history.cuh"
 
 namespace rocs {
@@ -16,63 +18,102 @@ namespace {
 
 template <int DH, typename T, int U>
 __global__ void __launch_bounds__(256) rocs_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int LPR = DH / 8, RPW = 32 / LPR;
+  constexpr int LPR = DH / 16, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31;
   int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (w >= p.warps) return;
   const int which = w >= p.warps0;
   const NormRopeSide& sd = p.side[which];
   if (which) w -= p.warps0;
-  const int t = (int)(w / sd.groups), h0 = (int)(w - (int64_t)t * sd.groups) * (RPW * U) + lane / LPR;
-  const int l = lane & (LPR - 1);
-  const T* x = static_cast<const T*>(sd.x) + (int64_t)t * sd.ld_x + (int64_t)h0 * DH + 8 * l;
-  float v[U][8];
+  const int l = lane % LPR;
+  const bool inter = p.interleaved, turned = p.rope && (inter ? 16 * l < p.rot : 8 * l < p.rot / 2);
+  int ch0, ch1;
+  groups_of(l, p.rope && !inter ? p.rot / 16 : 0, ch0, ch1);
+  const int64_t row0 = w * (RPW * U) + lane / LPR, rows = (int64_t)sd.n * sd.heads;
+  Raw8<T> raw[U][2];
+  int64_t at[U];  // the row's place in the output
+  int tok[U], pos[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[u][k] = 0.0f;
-    if (h0 + u * RPW < sd.heads) load8(x + u * RPW * DH, v[u]);
-  }
-  Rotation<DH> r;
-  if (p.rope) {
-    int pos = sd.pos[t];
-    if ((unsigned)pos >= (unsigned)p.max_pos) {
-      if (lane == 0) record_error(p.ws, ROCS_ERR_DEVICE_INDEX, 901);
-      pos = 0;
+    const int64_t row = row0 + u * RPW;
+    tok[u] = -1;
+    at[u] = 0;
+    if (row < rows) {
+      tok[u] = (int)((uint32_t)row / (uint32_t)sd.heads);
+      const int64_t in = (int64_t)(row - (int64_t)tok[u] * sd.heads) * DH;
+      at[u] = (int64_t)tok[u] * sd.ld_out + in;
+      const T* x = static_cast<const T*>(sd.x) + (int64_t)tok[u] * sd.ld_x + in;
+      raw[u][0].load(x + ch0);
+      raw[u][1].load(x + ch1);
+    } else {
+      raw[u][0].zero();
+      raw[u][1].zero();
     }
-    r.load(p.rope + (int64_t)pos * p.rot, p.rot, p.interleaved, lane);
+    pos[u] = p.rope && tok[u] >= 0 ? sd.pos[tok[u]] : 0;
   }
-  float g[8], b[8];
   const bool has_g = p.norm != ROCS_NORM_NONE && sd.gamma, has_b = p.norm != ROCS_NORM_NONE && sd.beta;
-  if (has_g) load8(sd.gamma + 8 * l, g);
-  if (has_b) load8(sd.beta + 8 * l, b);
-  T* out = static_cast<T*>(sd.out) + (int64_t)t * sd.ld_out + (int64_t)h0 * DH + 8 * l;
+  float g[16];
+  if (has_g) {
+    load8(sd.gamma + ch0, g);
+    load8(sd.gamma + ch1, g + 8);
+  }
+  Rotation r;
+  int held = -1;  // position that r is of
 #pragma unroll
   for (int u = 0; u < U; ++u) {
+    if (turned && (u == 0 || pos[u] != held)) {
+      held = pos[u];
+      int at_pos = held;
+      if ((unsigned)at_pos >= (unsigned)p.max_pos) {
+        record_error(p.ws, ROCS_ERR_DEVICE_INDEX, 901);
+        at_pos = 0;
+      }
+      r.load(p.rope + (int64_t)at_pos * p.rot, p.rot, l);
+    }
+    float v[16];
+    raw[u][0].get(v);
+    raw[u][1].get(v + 8);
     if (p.norm != ROCS_NORM_NONE) {
-      float mean = 0.0f;
       if (p.norm == ROCS_NORM_LAYER) {
         float s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += v[u][k];
-        mean = row_sum<LPR>(s) * (1.0f / DH);
-      }
-      float s = 0.0f;
+        for (int k = 0; k < 16; ++k) s += v[k];
+        const float mean = row_sum<LPR>(s) * (1.0f / DH);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[u][k] -= mean;
-        s = fmaf(v[u][k], v[u][k], s);
+        for (int k = 0; k < 16; ++k) v[k] -= mean;
       }
-      const float inv = 1.0f / sqrtf(row_sum<LPR>(s) * (1.0f / DH) + p.eps);
+      float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[u][k] *= inv;
-        if (has_g) v[u][k] *= g[k];
-        if (has_b) v[u][k] += b[k];
+      for (int k = 0; k < 16; k += 2) {
+        s0 = fmaf(v[k], v[k], s0);
+        s1 = fmaf(v[k + 1], v[k + 1], s1);
+      }
+      const float ms = row_sum<LPR>(s0 + s1) * (1.0f / DH) + p.eps;
+      // rsqrtf is off by 2 units of fp32 at most: nothing beside the rounding to bf16; fp32 outputs take the exact one
+      const float inv = sizeof(T) == 2 ? rsqrtf(ms) : 1.0f / sqrtf(ms);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] *= inv;
+      if (has_g) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] *= g[k];
+      }
+      if (has_b) {
+        float b[16];
+        load8(sd.beta + ch0, b);
+        load8(sd.beta + ch1, b + 8);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] += b[k];
       }
     }
-    if (p.rope) r.apply(v[u], p.interleaved, lane);
-    if (h0 + u * RPW < sd.heads) store8(out + u * RPW * DH, v[u]);
+    if (turned) {
+      if (inter) r.apply(v, true);
+      else r.apply(v, false);
+    }
+    if (tok[u] >= 0) {
+      T* out = static_cast<T*>(sd.out) + at[u];
+      store8(out + ch0, v);
+      store8(out + ch1, v + 8);
+    }
   }
 }
 
@@ -91,8 +132,7 @@ __global__ void rocs_rope_table_kernel(float* table, int64_t n, int half, double
 template <int DH, typename T>
 cudaError_t launch_nr(const NormRopeParams& p, int unroll, cudaStream_t st) {
   const unsigned grid = (unsigned)((p.warps + 7) / 8);
-  if (unroll == 4) rocs_norm_rope_kernel<DH, T, 4><<<grid, 256, 0, st>>>(p);
-  else if (unroll == 2) rocs_norm_rope_kernel<DH, T, 2><<<grid, 256, 0, st>>>(p);
+  if (unroll == 2) rocs_norm_rope_kernel<DH, T, 2><<<grid, 256, 0, st>>>(p);
   else rocs_norm_rope_kernel<DH, T, 1><<<grid, 256, 0, st>>>(p);
   return cudaGetLastError();
 }

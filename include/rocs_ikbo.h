@@ -457,7 +457,7 @@ ROCS_API int rocs_dca_forward_host(const rocs_dca_args* args, int64_t chunks, vo
  *       NULL: no rotation.  The first rot channels turn: channel i with i + rot/2, or, interleaved
  *       != 0, channel 2i with 2i + 1.  The others pass.  rot % 16 == 0, 0 < rot <= dh.
  * dtype ROCS_BF16 or ROCS_F32 (x and out); statistics and rotation in fp32, one rounding when
- * stored.  dh in {64, 128}; pointers 16-byte aligned, strides multiples of 16 bytes.  A position
+ * stored.  dh in {64, 128}; n * heads < 2^31; pointers 16-byte aligned, strides multiples of 16 bytes.  A position
  * outside [0, max_pos) sets ROCS_ERR_DEVICE_INDEX in the workspace status (that token's outputs are
  * undefined).  Workspace: 256 bytes.  One kernel launch.
  * ---------------------------------------------------------------------------------- */
@@ -499,7 +499,7 @@ ROCS_API int rocs_rope_table(float* table, int64_t max_pos, int64_t rot, double 
  * In each little-endian 32-bit word of codes (8 channels) nibble i of the low half is channel 2i,
  * nibble i of the high half channel 2i + 1.  A row with an infinity or a NaN in it, or whose range
  * passes fp32, is held with a NaN step and minimum and reads as NaN.
- * dh in {64, 128}; page in {16, 32, 64, 128}; pages * heads * page < 2^40; codes 16-byte and scale
+ * dh in {64, 128}; page in {16, 32, 64, 128}; pages * heads * page < 2^40, tokens of a call * heads < 2^31; codes 16-byte and scale
  * 16-byte aligned.
  * Page tables: [R, max_pages] int32; token j of request r is in page table[r, j / page].  Several
  * requests may share pages that are only read.
