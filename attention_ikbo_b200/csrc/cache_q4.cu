@@ -11,7 +11,7 @@
 // Each value is read once and leaves as 4 bits; a row's statistics are min and max over its dh/16 lanes.  The places of the
 // (at most 32) tokens are looked up once for the warp, a token to a lane.  The step is rounded to bf16 BEFORE the codes are
 // taken, so that codes are nearest to what they will stand for.  Memory bounds both directions; with one token to a warp and
-// a division for every value the two together took 129 us where they take APUS (8 histories of 4096-8192 events, 4 heads of
+// a division for every value the two together took 129 us where they take 84 us (8 histories of 4096-8192 events, 4 heads of
 // 128).
 #include "history.cuh"
 
@@ -48,11 +48,12 @@ __device__ __forceinline__ Place places(const CacheMoveParams& p, int t0, int n,
 
 template <int LPR>
 __device__ __forceinline__ void row_min_max(const float (&v)[16], float& lo, float& hi) {
-  lo = hi = v[0];
+  lo = fminf(v[0], v[1]);
+  hi = fmaxf(v[0], v[1]);
 #pragma unroll
-  for (int k = 1; k < 16; ++k) {
-    lo = fminf(lo, v[k]);
-    hi = fmaxf(hi, v[k]);
+  for (int k = 2; k < 16; k += 2) {
+    asm("min.f32 %0, %0, %1, %2;" : "+f"(lo) : "f"(v[k]), "f"(v[k + 1]));
+    asm("max.f32 %0, %0, %1, %2;" : "+f"(hi) : "f"(v[k]), "f"(v[k + 1]));
   }
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) {
@@ -61,29 +62,35 @@ __device__ __forceinline__ void row_min_max(const float (&v)[16], float& lo, flo
   }
 }
 
-// Codes of 8 values, packed: rint((x - mn) / step) held to 0 ... 15.  The quotient by a reciprocal is off by at most 2^-22 of
-// itself, so it rounds as the exact one does unless it lies within 2e-5 of a half; then (rare) the values are divided.
+// Codes of 8 values, packed: rint((x - mn) / step), held to 0 ... 15 where CLAMP.  The quotient by the reciprocal is
+// corrected with its own remainder (exact, a fused multiply-add), which rounds it as the division does; bf16 values lie on a
+// grid, so quotients of exactly a half are common and have to come out as such.
+template <bool CLAMP>
 __device__ __forceinline__ uint32_t codes8(const float* v, float mn, float step, float inv) {
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it rounds to a whole number, half to even
-  float c[8], far = 0.0f;
+  const uint64_t mn2 = pack2(-mn, -mn), step2 = pack2(-step, -step), inv2 = pack2(inv, inv);
+  // adding 1.5 * 2^23 rounds to a whole number, half to even, and leaves it in the low bits
+  const uint64_t round2 = pack2(12582912.0f, 12582912.0f);
+  uint32_t c[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float t = fminf(fmaxf((v[k] - mn) * inv, 0.0f), 15.0f);
-    c[k] = __fsub_rn(__fadd_rn(t, kRound), kRound);
-    far = fmaxf(far, fabsf(t - c[k]));
+  for (int k = 0; k < 8; k += 2) {
+    const uint64_t d = add2(pack2(v[k], v[k + 1]), mn2), t = mul2(d, inv2);
+    uint64_t q = fma2(fma2(t, step2, d), inv2, t);
+    float a, b;
+    if (CLAMP) {
+      unpack2(q, a, b);
+      q = pack2(fminf(fmaxf(a, 0.0f), 15.0f), fminf(fmaxf(b, 0.0f), 15.0f));
+    }
+    unpack2(add2(q, round2), a, b);
+    c[k] = __float_as_uint(a);
+    c[k + 1] = __float_as_uint(b);
   }
-  if (far > 0.49998f) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) c[k] = fminf(fmaxf(rintf(__fdiv_rn(v[k] - mn, step)), 0.0f), 15.0f);
-  }
-  // whole numbers below 2^16 in fp32 are exact, and 2^23 more leaves them in the low bits
-  const float even = fmaf(4096.0f, c[6], fmaf(256.0f, c[4], fmaf(16.0f, c[2], c[0]))) + 8388608.0f;
-  const float odd = fmaf(4096.0f, c[7], fmaf(256.0f, c[5], fmaf(16.0f, c[3], c[1]))) + 8388608.0f;
-  return __byte_perm(__float_as_uint(even), __float_as_uint(odd), 0x5410);
+  // the low halves of the words of 1.5 * 2^23 are zero: only codes meet there
+  const uint32_t even = c[0] + (c[2] << 4) + (c[4] << 8) + (c[6] << 12), odd = c[1] + (c[3] << 4) + (c[5] << 8) + (c[7] << 12);
+  return __byte_perm(even, odd, 0x5410);
 }
 
 template <int DH, typename T, int U>
-__global__ void __launch_bounds__(256) rocs_cache_append_kernel(const __grid_constant__ CacheMoveParams p) {
+__global__ void __launch_bounds__(256, 4) rocs_cache_append_kernel(const __grid_constant__ CacheMoveParams p) {
   constexpr int LPR = DH / 16, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, l = lane % LPR;
   int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -146,29 +153,40 @@ __global__ void __launch_bounds__(256) rocs_cache_append_kernel(const __grid_con
     }
     float lo, hi;
     row_min_max<LPR>(v, lo, hi);
-    bool bad = false;  // min and max pass over NaN
+    uint64_t z = 0;  // min and max pass over NaN; times zero and summed it stays (and an infinity becomes one)
 #pragma unroll
-    for (int k = 0; k < 16; ++k) bad |= v[k] != v[k];
-    const unsigned any = __ballot_sync(0xffffffffu, bad);
+    for (int k = 0; k < 16; k += 2) z = fma2(pack2(v[k], v[k + 1]), 0, z);
+    float z0, z1;
+    unpack2(z, z0, z1);
+    const unsigned any = __ballot_sync(0xffffffffu, !(z0 + z1 == 0.0f));
     const float range = hi - lo;
     const unsigned mine = ((1u << LPR) - 1) << (lane & ~(LPR - 1));
     const bool finite = range < INFINITY && !(any & mine);  // false too where range is NaN
-    const __nv_bfloat162 sc = __floats2bfloat162_rn(finite ? __fdiv_rn(range, 15.0f) : NAN, finite ? lo : NAN);
+    // range / 15 rounded as the division does, by the same correction
+    const float r15 = range * (1.0f / 15.0f), fifteenth = fmaf(fmaf(r15, -15.0f, range), 1.0f / 15.0f, r15);
+    const __nv_bfloat162 sc = __floats2bfloat162_rn(finite ? (range > 1e-30f && range < 1e36f ? fifteenth : range / 15.0f) : NAN,
+                                                    finite ? lo : NAN);
     const float step = __low2float(sc), mn = __high2float(sc);
     uint32_t w0 = 0, w1 = 0;
-    if (step > 0.0f) {
-      // a step whose reciprocal is not a normal number takes the division for every value
-      const float inv = step > 1e-37f && step < 1e37f ? 1.0f / step : NAN;
-      if (inv == inv) {
-        w0 = codes8(v, mn, step, inv);
-        w1 = codes8(v + 8, mn, step, inv);
+    if (step > 1e-36f && step < 1e36f) {
+      const float inv = 1.0f / step;
+      // the row's ends say whether a value can pass 0 ... 15 (the minimum was rounded up, or the step down)
+      if ((lo - mn) * inv > -0.49f && (hi - mn) * inv < 15.49f) {
+        w0 = codes8<false>(v, mn, step, inv);
+        w1 = codes8<false>(v + 8, mn, step, inv);
       } else {
+        w0 = codes8<true>(v, mn, step, inv);
+        w1 = codes8<true>(v + 8, mn, step, inv);
+      }
+    } else if (step > 0.0f) {  // so small or large that the reciprocal is no normal number
+#pragma unroll 1
+      for (int k = 0; k < 16; ++k) {
+        float x = v[0];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const uint32_t c = (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(v[k] - mn, step)), 0.0f), 15.0f) << (4 * ((k & 7) >> 1) + 16 * (k & 1));
-          if (k < 8) w0 |= c;
-          else w1 |= c;
-        }
+        for (int i = 1; i < 16; ++i) x = k == i ? v[i] : x;
+        const uint32_t c = (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(x - mn, step)), 0.0f), 15.0f) << (4 * ((k & 7) >> 1) + 16 * (k & 1));
+        if (k < 8) w0 |= c;
+        else w1 |= c;
       }
     }
     if (tok[u] >= 0 && place >= 0) {
@@ -214,13 +232,14 @@ __global__ void __launch_bounds__(256) rocs_cache_read_kernel(const __grid_const
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (to[u] < 0) continue;
-    const float step = __low2float(sc[u]), mn = __high2float(sc[u]);
-    float v[16];
+    const uint32_t rsc = *reinterpret_cast<const uint32_t*>(&sc[u]);
+    const uint32_t st = __byte_perm(rsc, rsc, 0x1010), mn = __byte_perm(rsc, rsc, 0x3232);
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      v[k] = fmaf(step, (float)(((k < 8 ? code[u].x : code[u].y) >> (4 * ((k & 7) >> 1) + 16 * (k & 1))) & 15u), mn);
-    store8(out + to[u], v);
-    store8(out + to[u] + 8, v + 8);
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t c = k ? code[u].y : code[u].x;
+      st_global_v4(out + to[u] + 8 * k, value2(pair16<0>(c), st, mn), value2(pair16<1>(c), st, mn), value2(pair16<2>(c), st, mn),
+                   value2(pair16<3>(c), st, mn));
+    }
   }
 }
 

@@ -127,20 +127,6 @@ struct Work {
   __device__ __forceinline__ int last_cta() const { return (int)((pos - step + steps - 1) / share); }
 };
 
-// pair i of a word of codes as bf16 (16 + low, 16 + high): the nibbles moved to the top mantissa bits under the
-// exponent of 16
-template <int I>
-__device__ __forceinline__ uint32_t pair16(uint32_t w) {
-  const uint32_t s = I == 0 ? w << 3 : I == 1 ? w >> 1 : I == 2 ? w >> 5 : w >> 9;
-  return (s & 0x00780078u) | 0x41804180u;
-}
-// such a pair as values, minimum + step * code, each rounded once
-__device__ __forceinline__ uint32_t value2(uint32_t c16, uint32_t step, uint32_t mn) {
-  uint32_t c, r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(c16), "r"(0x41804180u));  // exact
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(step), "r"(mn));
-  return r;
-}
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 // mbar_wait that sleeps between polls.  A failed poll comes back after some 40 cycles and costs about ten instructions;

