@@ -8,16 +8,23 @@
 // and unpacking costs a shift and one three-input logic operation for two values.  Scores are exact up to fp32 sums;
 // the one rounding to fewer bits is that of P' (it multiplies codes on the tensor core in bf16).
 //
-// With at most 16 rows to a pair of (request, key head) each 4-bit value is used 16 times at most: the bytes of the
-// cache bound it.  mma.sync (16 rows x 8 keys) takes its operands from registers, so codes go from shared memory
-// through the logic operations straight into fragments, with no second trip through shared memory as a tcgen05 operand
-// tile would need, and 16 rows fill an instruction where a tcgen05 tile has at least 64.  Each warp takes 16 keys at a
-// time through its own ring of cp.async stages (a 16-key granule never crosses a page) with its own running softmax:
-// no block-wide synchronisation until the unit's end, where the four warps' results are joined in shared memory.
+// With a few rows to a pair of (request, key head) each 4-bit value is used a few times: the bytes of the cache and the
+// unpacking bound it.  mma.sync takes its operands from registers, so codes go from shared memory through the logic
+// operations straight into fragments, with no second trip through shared memory as a tcgen05 operand tile would need.
+// Keys (in Q K^T) and channels (in P V) are the instruction's 16 rows and query rows its 8 columns, so 8 rows fill it,
+// where a tcgen05 tile has at least 64: S^T = K Q^T, O^T = V^T P^T, and an 8 x 8 transposition (movmatrix) turns S^T's
+// layout into that of P^T.  NB = 1 or 2 blocks of 8 rows share the unpacked codes.  With query rows as the 16 rows of the
+// instruction (8 keys or channels to each) it issued twice the products and exponentials for up to 8 rows, and took 204
+// us where this takes 154 us (32 histories of 8192-16384 keys, 8 heads of 128, 4 rows).
+//
+// Each warp takes 16 keys at a time through its own ring of cp.async stages (a 16-key granule never crosses a page) with its
+// own running softmax: no block-wide synchronisation until the unit's end, where the four warps' results are joined in
+// shared memory.  A row's maximum is only taken where a score passes the running one by more than 2^8 (a vote finds that).
 //
 // Fragments without shuffles: the contraction index may be permuted freely as long as both operands agree.  Lane
-// (g, t) = (lane / 4, lane % 4) owns channels t*DH/4 ... of key g in Q K^T (one 16-byte load), and channels
-// g*DH/8 ... of its keys in P V, which leaves it with DH/4 contiguous channels of O for rows g and g + 8.
+// (g, t) = (lane / 4, lane % 4) owns channels t*DH/4 ... of keys g and g + 8 (and of query row g) in Q K^T, and channels
+// g*DH/8 ... of its keys 2t, 2t + 1, 2t + 8, 2t + 9 in P V, which leaves it with DH/8 contiguous channels of O for rows 2t
+// and 2t + 1.
 #include "cache_work.cuh"
 
 namespace rocs {
@@ -26,12 +33,12 @@ namespace {
 
 constexpr int kWarps = 4, kThreadsFew = kWarps * 32, kStages = 4, kGran = 16, kKeys = kWarps * kGran;
 
-template <int DH>
+template <int DH, int NB>
 struct FewSmem {
   static constexpr int kRow = DH / 2;                         // bytes of codes in a row
   static constexpr int kStage = 2 * kGran * kRow + 2 * kGran * 4;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kMerge = kWarps * kFewRows * (DH + 4) * 4;  // O of every warp (rows padded by 16 bytes)
+  static constexpr int kMerge = kWarps * 8 * NB * (DH + 4) * 4;  // O of every warp (rows padded by 16 bytes)
   static constexpr int kBuf = kRing > kMerge ? kRing : kMerge;
 };
 template <int DH>
@@ -56,37 +63,40 @@ __device__ __forceinline__ float quad_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-template <int DH>
-__global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __grid_constant__ CacheAttnParams p) {
-  using L = FewSmem<DH>;
-  constexpr int KS = DH / 16;   // contraction steps of Q K^T
-  constexpr int NT = DH / 8;    // 8-channel tiles of O
-  constexpr int CH = DH / 4;    // channels of a row that a lane holds
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // of an 8 x 8 matrix of 16-bit values over the warp
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int DH, int NB>
+__global__ void __launch_bounds__(kThreadsFew, NB == 1 ? 5 : 3) rocs_cache_few_kernel(const __grid_constant__ CacheAttnParams p) {
+  using L = FewSmem<DH, NB>;
+  constexpr int KS = DH / 16;   // contraction steps of Q K^T, and 16-channel tiles of O
+  constexpr int CH = DH / 4;    // channels of a row that a lane holds in Q K^T
+  constexpr int OC = DH / 8;    // channels of O that a lane holds
+  constexpr int kRows = 8 * NB;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][kFewRows], s_l[kWarps][kFewRows];
+  __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ int64_t s_sum[33], s_out[3];
   __shared__ int s_last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   Work<kKeys> w;
-  if (!w.start(p, kFewRows, s_sum, s_out, 2)) return;
+  if (!w.start(p, kRows, s_sum, s_out, 2)) return;
   const uint32_t ring = smem_u32(smem) + warp * (kStages * L::kStage);
-  // keys of a granule's half that this lane's score columns are (and its V rows): neighbours, in an order that spreads
-  // the four lanes' V rows over all banks
-  const int ka = (2 * t) ^ (t >> 1), kb = ka ^ 1;
   const float c = p.scale_log2;
 
   for (bool more = true; more;) {
     const Request& q = w.q;
-    const int row0 = w.chunk * kFewRows, n_steps = w.count();
+    const int row0 = w.chunk * kRows, n_steps = w.count();
     const int tpr = p.G;  // rows of one token
-    // Q fragments: rows g and g + 8, this lane's CH channels
-    uint32_t qa[KS][4];
-    float qsum[2];
-    int lim[2];
+    // Q fragments: row g of each block, this lane's CH channels; sums and limits of rows 2t and 2t + 1
+    uint32_t qb[NB][KS][2];
+    float qsum[NB][2];
+    int lim[NB][2], lim_min = q.L;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = row0 + g + 8 * i;
-      lim[i] = row_limit(p, q, row);
+    for (int b = 0; b < NB; ++b) {
+      const int row = row0 + 8 * b + g;
       const int tok = row < q.rows ? row / tpr : 0, hh = w.head * p.G + (row < q.rows ? row - tok * tpr : 0);
       const int64_t token = (int64_t)q.c0 * p.q_tokens + tok;
       const uint4* src = reinterpret_cast<const uint4*>(p.q + token * p.q_ld + (int64_t)hh * DH + t * CH);
@@ -95,23 +105,36 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
       for (int k = 0; k < CH / 8; ++k) {
         uint4 u = make_uint4(0, 0, 0, 0);
         if (row < q.rows) u = src[k];
-        qa[2 * k][i] = u.x;
-        qa[2 * k][2 + i] = u.y;
-        qa[2 * k + 1][i] = u.z;
-        qa[2 * k + 1][2 + i] = u.w;
+        qb[b][2 * k][0] = u.x;
+        qb[b][2 * k][1] = u.y;
+        qb[b][2 * k + 1][0] = u.z;
+        qb[b][2 * k + 1][1] = u.w;
         s += (bf_lo(u.x) + bf_hi(u.x)) + (bf_lo(u.y) + bf_hi(u.y)) + (bf_lo(u.z) + bf_hi(u.z)) + (bf_lo(u.w) + bf_hi(u.w));
       }
-      qsum[i] = quad_sum(s);
+      s = quad_sum(s);
+      const int mine = row_limit(p, q, row);
+      lim_min = min(lim_min, mine);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // row 2t + e is that of lanes with g = 2t + e
+        qsum[b][e] = __shfl_sync(0xffffffffu, s, 4 * (2 * t + e));
+        lim[b][e] = __shfl_sync(0xffffffffu, mine, 4 * (2 * t + e));
+      }
     }
-    int lim_min = min(lim[0], lim[1]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
+    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
 
-    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f}, corr[2] = {0.0f, 0.0f};
+    float o[NB][KS][4], m[NB][2], l[NB][2], corr[NB][2];
 #pragma unroll
-    for (int k = 0; k < NT; ++k)
+    for (int b = 0; b < NB; ++b) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[k][i] = 0.0f;
+      for (int e = 0; e < 2; ++e) {
+        m[b][e] = -INFINITY;
+        l[b][e] = corr[b][e] = 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[b][k][i] = 0.0f;
+    }
 
     // this warp's granules: step*4 + warp, those with keys in them
     const int first = w.step * kWarps + warp, all = (q.L + kGran - 1) / kGran;
@@ -158,103 +181,106 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
       issue(i + kStages - 1, pg);
       const uint32_t st = ring + (i % kStages) * L::kStage;
       const int key0 = (first + i * kWarps) * kGran;
-      // scores of 2 x 8 keys
-      float s[2][4];
+      // scores: keys g and g + 8, rows 2t and 2t + 1 of each block
+      float s[NB][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
-        const int key = 8 * j + (g ^ ((g >> 2) & 1));
-        uint32_t cw[CH / 8];
-        if constexpr (DH == 128) {
-          const uint4 u = ld_shared_v4(st + key * L::kRow + ((t ^ (key & 2)) << 4));
-          cw[0] = u.x; cw[1] = u.y; cw[2] = u.z; cw[3] = u.w;
-        } else {
-          asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(cw[0]), "=r"(cw[1]) : "r"(st + key * L::kRow + (t << 3)) : "memory");
+      for (int b = 0; b < NB; ++b) s[b][0] = s[b][1] = s[b][2] = s[b][3] = 0.0f;
+      {
+        uint32_t cw[2][CH / 8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int key = g + 8 * h;
+          if constexpr (DH == 128) {
+            const uint4 u = ld_shared_v4(st + key * L::kRow + ((t ^ (key & 2)) << 4));
+            cw[h][0] = u.x; cw[h][1] = u.y; cw[h][2] = u.z; cw[h][3] = u.w;
+          } else {
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(cw[h][0]), "=r"(cw[h][1]) : "r"(st + key * L::kRow + (t << 3)) : "memory");
+          }
         }
 #pragma unroll
         for (int k = 0; k < KS / 2; ++k) {
-          mma16816(s[j], qa[2 * k], pair16<0>(cw[k]), pair16<1>(cw[k]));
-          mma16816(s[j], qa[2 * k + 1], pair16<2>(cw[k]), pair16<3>(cw[k]));
+          const uint32_t a0[4] = {pair16<0>(cw[0][k]), pair16<0>(cw[1][k]), pair16<1>(cw[0][k]), pair16<1>(cw[1][k])};
+          const uint32_t a1[4] = {pair16<2>(cw[0][k]), pair16<2>(cw[1][k]), pair16<3>(cw[0][k]), pair16<3>(cw[1][k])};
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            mma16816(s[b], a0, qb[b][2 * k][0], qb[b][2 * k][1]);
+            mma16816(s[b], a1, qb[b][2 * k + 1][0], qb[b][2 * k + 1][1]);
+          }
         }
       }
-      // x = log2-domain scores; steps and minima of this lane's 4 keys
-      uint32_t sk[4], sv[4];
+      // x = log2-domain scores
+      uint32_t sk[2], sv[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t at = st + 2 * kGran * L::kRow + (8 * j + 2 * t) * 4;
-        uint32_t a, b;
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at) : "memory");
-        sk[2 * j] = t < 2 ? a : b;
-        sk[2 * j + 1] = t < 2 ? b : a;
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(at + kGran * 4) : "memory");
-        sv[2 * j] = t < 2 ? a : b;
-        sv[2 * j + 1] = t < 2 ? b : a;
+      for (int h = 0; h < 2; ++h) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sk[h]) : "r"(st + 2 * kGran * L::kRow + (g + 8 * h) * 4) : "memory");
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sv[h]) : "r"(st + 2 * kGran * L::kRow + (kGran + g + 8 * h) * 4) : "memory");
       }
       const bool cut = key0 + kGran > lim_min;  // some row does not see some key of the granule
-      float mx[2] = {-INFINITY, -INFINITY};
+      bool grown = false;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int h = 0; h < 2; ++h) {
+        const float a = c * bf_lo(sk[h]), d = fmaf(-16.0f, a, c * bf_hi(sk[h]));
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float a = c * bf_lo(sk[2 * j + e]), b = fmaf(-16.0f, a, c * bf_hi(sk[2 * j + e]));
-          const int key = key0 + 8 * j + (e ? kb : ka);
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2) {
-            float x = fmaf(a, s[j][2 * i2 + e], b * qsum[i2]);
-            if (cut && key >= lim[i2]) x = -INFINITY;
-            s[j][2 * i2 + e] = x;
-            mx[i2] = fmaxf(mx[i2], x);
+          for (int e = 0; e < 2; ++e) {
+            float x = fmaf(a, s[b][2 * h + e], d * qsum[b][e]);
+            if (cut && key0 + g + 8 * h >= lim[b][e]) x = -INFINITY;
+            s[b][2 * h + e] = x;
+            grown |= x > m[b][e] + 8.0f;
           }
-        }
-#pragma unroll
-      for (int i2 = 0; i2 < 2; ++i2) {
-        mx[i2] = fmaxf(mx[i2], __shfl_xor_sync(0xffffffffu, mx[i2], 1));
-        mx[i2] = fmaxf(mx[i2], __shfl_xor_sync(0xffffffffu, mx[i2], 2));
       }
       // O and the sums move to a new maximum only where it grew by more than 2^8 (P stays far below overflow)
-      if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.0f || mx[1] > m[1] + 8.0f)) {
-        float f[2];
+      if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          const float mn = fmaxf(m[i2], mx[i2]);
-          f[i2] = mn == -INFINITY ? 1.0f : ex2(m[i2] - mn);
-          m[i2] = mn;
-          l[i2] *= f[i2];
-          corr[i2] *= f[i2];
-        }
+        for (int b = 0; b < NB; ++b) {
+          float f[2];
 #pragma unroll
-        for (int k = 0; k < NT; ++k) {
-          o[k][0] *= f[0];
-          o[k][1] *= f[0];
-          o[k][2] *= f[1];
-          o[k][3] *= f[1];
+          for (int e = 0; e < 2; ++e) {
+            float mx = fmaxf(m[b][e], fmaxf(s[b][e], s[b][2 + e]));
+#pragma unroll
+            for (int i2 = 4; i2 < 32; i2 *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i2));
+            f[e] = mx == -INFINITY ? 1.0f : ex2(m[b][e] - mx);
+            m[b][e] = mx;
+            l[b][e] *= f[e];
+            corr[b][e] *= f[e];
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            o[b][k][0] *= f[0];
+            o[b][k][1] *= f[1];
+            o[b][k][2] *= f[0];
+            o[b][k][3] *= f[1];
+          }
         }
       }
-      uint32_t pa[4];
-      const float mu[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+      uint32_t pb[NB][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int b = 0; b < NB; ++b) {
+        const float mu[2] = {m[b][0] == -INFINITY ? 0.0f : m[b][0], m[b][1] == -INFINITY ? 0.0f : m[b][1]};
 #pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          const float p0 = ex2(s[j][2 * i2] - mu[i2]), p1 = ex2(s[j][2 * i2 + 1] - mu[i2]);
-          l[i2] += p0 + p1;
-          float w0 = p0 * bf_lo(sv[2 * j]), w1 = p1 * bf_lo(sv[2 * j + 1]);
-          float c0 = p0 * bf_hi(sv[2 * j]), c1 = p1 * bf_hi(sv[2 * j + 1]);
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = ex2(s[b][2 * h] - mu[0]), p1 = ex2(s[b][2 * h + 1] - mu[1]);
+          l[b][0] += p0;
+          l[b][1] += p1;
+          float w0 = p0 * bf_lo(sv[h]), w1 = p1 * bf_lo(sv[h]), c0 = p0 * bf_hi(sv[h]), c1 = p1 * bf_hi(sv[h]);
           if (cut) {  // a key that the row does not see counts for nothing, whatever its scale holds
-            if (key0 + 8 * j + ka >= lim[i2]) w0 = c0 = 0.0f;
-            if (key0 + 8 * j + kb >= lim[i2]) w1 = c1 = 0.0f;
+            if (key0 + g + 8 * h >= lim[b][0]) w0 = c0 = 0.0f;
+            if (key0 + g + 8 * h >= lim[b][1]) w1 = c1 = 0.0f;
           }
           const uint32_t pk = pack_bf16x2(w0, w1);
-          pa[2 * j + i2] = pk;
-          corr[i2] += fmaf(-16.0f, bf_lo(pk) + bf_hi(pk), c0 + c1);
+          corr[b][0] += fmaf(-16.0f, bf_lo(pk), c0);
+          corr[b][1] += fmaf(-16.0f, bf_hi(pk), c1);
+          pb[b][h] = transpose8(pk);
         }
-      // P V: keys ka, kb of both halves; this lane's DH/8 channels of each
+      }
+      // P V: keys 2t, 2t + 1 of both halves; this lane's DH/8 channels of each
       const uint32_t vst = st + kGran * L::kRow;
       constexpr int VW = DH / 64;  // words of DH/8 channels
       uint32_t v[4][VW];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int key = 8 * (e >> 1) + ((e & 1) ? kb : ka);
+        const int key = 8 * (e >> 1) + 2 * t + (e & 1);
         if constexpr (DH == 128)
           asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[e][0]), "=r"(v[e][VW - 1])
                        : "r"(vst + key * L::kRow + (((g >> 1) ^ (key & 2)) << 4) + ((g & 1) << 3)) : "memory");
@@ -265,42 +291,49 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
       for (int k = 0; k < VW; ++k) {
         const uint32_t lo0 = __byte_perm(v[0][k], v[1][k], 0x5410), hi0 = __byte_perm(v[0][k], v[1][k], 0x7632);
         const uint32_t lo1 = __byte_perm(v[2][k], v[3][k], 0x5410), hi1 = __byte_perm(v[2][k], v[3][k], 0x7632);
-        mma16816(o[8 * k + 0], pa, pair16<0>(lo0), pair16<0>(lo1));
-        mma16816(o[8 * k + 1], pa, pair16<0>(hi0), pair16<0>(hi1));
-        mma16816(o[8 * k + 2], pa, pair16<1>(lo0), pair16<1>(lo1));
-        mma16816(o[8 * k + 3], pa, pair16<1>(hi0), pair16<1>(hi1));
-        mma16816(o[8 * k + 4], pa, pair16<2>(lo0), pair16<2>(lo1));
-        mma16816(o[8 * k + 5], pa, pair16<2>(hi0), pair16<2>(hi1));
-        mma16816(o[8 * k + 6], pa, pair16<3>(lo0), pair16<3>(lo1));
-        mma16816(o[8 * k + 7], pa, pair16<3>(hi0), pair16<3>(hi1));
+        // tile 4k + i: channels 2i (its rows 0-7) and 2i + 1 (8-15) of the word, two keys to a register
+        const uint32_t a0[4] = {pair16<0>(lo0), pair16<0>(hi0), pair16<0>(lo1), pair16<0>(hi1)};
+        const uint32_t a1[4] = {pair16<1>(lo0), pair16<1>(hi0), pair16<1>(lo1), pair16<1>(hi1)};
+        const uint32_t a2[4] = {pair16<2>(lo0), pair16<2>(hi0), pair16<2>(lo1), pair16<2>(hi1)};
+        const uint32_t a3[4] = {pair16<3>(lo0), pair16<3>(hi0), pair16<3>(lo1), pair16<3>(hi1)};
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          mma16816(o[b][4 * k + 0], a0, pb[b][0], pb[b][1]);
+          mma16816(o[b][4 * k + 1], a1, pb[b][0], pb[b][1]);
+          mma16816(o[b][4 * k + 2], a2, pb[b][0], pb[b][1]);
+          mma16816(o[b][4 * k + 3], a3, pb[b][0], pb[b][1]);
+        }
       }
     }
     cp_wait<0>();
     __syncthreads();  // the ring becomes the merge buffer
-    // lane (g, t): tile n holds O of channels 2t*NT + n and (2t+1)*NT + n, rows g and g + 8
-    float* mine = reinterpret_cast<float*>(smem) + warp * kFewRows * (DH + 4);
+    // lane (g, t): rows 2t and 2t + 1 of each block, channels g*OC ...: tile k holds channels 2k and 2k + 1 of them
+    float* mine = reinterpret_cast<float*>(smem) + warp * kRows * (DH + 4);
 #pragma unroll
-    for (int i2 = 0; i2 < 2; ++i2) {
-      l[i2] = quad_sum(l[i2]);
-      corr[i2] = quad_sum(corr[i2]);
-      float* dst = mine + (g + 8 * i2) * (DH + 4) + t * CH;
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int k = 0; k < NT; k += 4)
-          *reinterpret_cast<float4*>(dst + e * NT + k) =
-              make_float4(o[k][2 * i2 + e] + corr[i2], o[k + 1][2 * i2 + e] + corr[i2], o[k + 2][2 * i2 + e] + corr[i2],
-                          o[k + 3][2 * i2 + e] + corr[i2]);
-      if (t == 0) {
-        s_m[warp][g + 8 * i2] = m[i2];
-        s_l[warp][g + 8 * i2] = l[i2];
+        for (int i2 = 4; i2 < 32; i2 *= 2) {
+          l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], i2);
+          corr[b][e] += __shfl_xor_sync(0xffffffffu, corr[b][e], i2);
+        }
+        const int row = 8 * b + 2 * t + e;
+        float* dst = mine + row * (DH + 4) + g * OC;
+#pragma unroll
+        for (int k = 0; k < KS; k += 2)
+          *reinterpret_cast<float4*>(dst + 2 * k) = make_float4(o[b][k][e] + corr[b][e], o[b][k][2 + e] + corr[b][e],
+                                                                o[b][k + 1][e] + corr[b][e], o[b][k + 1][2 + e] + corr[b][e]);
+        if (g == 0) {
+          s_m[warp][row] = m[b][e];
+          s_l[warp][row] = l[b][e];
+        }
       }
-    }
     __syncthreads();
-    // 8 threads to a row, DH/8 channels each
+    // kTpr threads to a row, TC channels each
     {
-      constexpr int TC = DH / 8;
-      const int row = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * TC;
+      constexpr int kTpr = kThreadsFew / kRows, TC = DH / kTpr;
+      const int row = threadIdx.x / kTpr, d0 = (threadIdx.x % kTpr) * TC;
       float mm = -INFINITY, ll = 0.0f, acc[TC];
 #pragma unroll
       for (int k = 0; k < TC; ++k) acc[k] = 0.0f;
@@ -311,7 +344,7 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
         const float f = mm == -INFINITY ? 0.0f : ex2(s_m[x][row] - mm);
         // a warp without a key for the row has l = 0 and O = 0 (m = -inf, f = 0), but NaN must not be lost
         ll += f * s_l[x][row];
-        const float* src = reinterpret_cast<const float*>(smem) + (x * kFewRows + row) * (DH + 4) + d0;
+        const float* src = reinterpret_cast<const float*>(smem) + (x * kRows + row) * (DH + 4) + d0;
 #pragma unroll
         for (int k = 0; k < TC; k += 4) {
           const float4 v4 = *reinterpret_cast<const float4*>(src + k);
@@ -329,7 +362,7 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
 #pragma unroll
         for (int k = 0; k < TC; k += 4)
           __stcg(reinterpret_cast<float4*>(dst + row * DH + d0 + k), make_float4(acc[k], acc[k + 1], acc[k + 2], acc[k + 3]));
-        if ((threadIdx.x & 7) == 0) {
+        if (threadIdx.x % kTpr == 0) {
           __stcg(dst + kFewRows * DH + row, mm);
           __stcg(dst + kFewRows * DH + kFewRows + row, ll);
         }
@@ -370,10 +403,9 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
         __nv_bfloat16* dst = p.o + at * DH + d0;
 #pragma unroll
-        for (int k = 0; k < TC; k += 8)
-          st_global_v4(dst + k, pack_bf16x2(acc[k] * inv, acc[k + 1] * inv), pack_bf16x2(acc[k + 2] * inv, acc[k + 3] * inv),
-                       pack_bf16x2(acc[k + 4] * inv, acc[k + 5] * inv), pack_bf16x2(acc[k + 6] * inv, acc[k + 7] * inv));
-        if (p.lse && (threadIdx.x & 7) == 0) p.lse[at] = ll == 0.0f ? -INFINITY : (mm + lg2(ll)) * kLn2;
+        for (int k = 0; k < TC; k += 4)
+          *reinterpret_cast<uint2*>(dst + k) = make_uint2(pack_bf16x2(acc[k] * inv, acc[k + 1] * inv), pack_bf16x2(acc[k + 2] * inv, acc[k + 3] * inv));
+        if (p.lse && threadIdx.x % kTpr == 0) p.lse[at] = ll == 0.0f ? -INFINITY : (mm + lg2(ll)) * kLn2;
       }
     }
     __syncthreads();  // the merge buffer becomes the ring again
@@ -381,23 +413,24 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
   }
 }
 
-template <int DH>
+template <int DH, int NB>
 cudaError_t launch_few(const CacheAttnParams& p, int grid, cudaStream_t st) {
   static std::atomic<uint64_t> optin_done{0};
-  auto k = rocs_cache_few_kernel<DH>;
-  const cudaError_t e = ensure_smem_optin(optin_done, k, FewSmem<DH>::kBuf);
+  auto k = rocs_cache_few_kernel<DH, NB>;
+  const cudaError_t e = ensure_smem_optin(optin_done, k, FewSmem<DH, NB>::kBuf);
   if (e != cudaSuccess) return e;
-  k<<<grid, kThreadsFew, FewSmem<DH>::kBuf, st>>>(p);
+  k<<<grid, kThreadsFew, FewSmem<DH, NB>::kBuf, st>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-int cache_few_grid(int sms) { return 3 * sms; }
+int cache_few_grid(int sms, int rows) { return (rows <= 8 ? 5 : 3) * sms; }
 size_t cache_few_part_bytes(int dh) { return (size_t)(dh == 128 ? few_part<128>() : few_part<64>()) * sizeof(float); }
 
-cudaError_t launch_cache_few(const CacheAttnParams& p, int dh, int grid, cudaStream_t st) {
-  return dh == 128 ? launch_few<128>(p, grid, st) : launch_few<64>(p, grid, st);
+cudaError_t launch_cache_few(const CacheAttnParams& p, int dh, int rows, int grid, cudaStream_t st) {
+  if (rows <= 8) return dh == 128 ? launch_few<128, 1>(p, grid, st) : launch_few<64, 1>(p, grid, st);
+  return dh == 128 ? launch_few<128, 2>(p, grid, st) : launch_few<64, 2>(p, grid, st);
 }
 
 }  // namespace rocs

@@ -183,6 +183,7 @@ inline size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
 struct AttnPlan {
   int64_t C = 0;
   int rows_hi = 0;  // requests with up to this many rows go to the kernel for few rows
+  int rows_few = 0;  // the most that a request of the kernel for few rows has
   int grid_few = 0, grid_many = 0;  // 0: not launched
   size_t cnt_many = 0, zero = 0, bytes = 0;
 };
@@ -210,11 +211,14 @@ int attn_validate(const rocs_dca_cache_args* a, AttnPlan* pl) {
     if (a->q_ld % 8 || a->q_ld >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
     const int64_t G = a->H / a->cache.heads;
     pl->rows_hi = G > kMaxShared ? 0x7fffffff : kFewLimit;
-    for (int64_t r = 0; r < a->R && (!pl->grid_few || !pl->grid_many); ++r) {
+    for (int64_t r = 0; r < a->R; ++r) {
       const int64_t rows = (a->cand_off_host[r + 1] - a->cand_off_host[r]) * a->q * G;
-      if (rows > pl->rows_hi) pl->grid_many = sm_count_ext();
-      else if (rows > 0) pl->grid_few = cache_few_grid(sm_count_ext());
+      if (rows > pl->rows_hi) pl->grid_many = 1;
+      else if (rows > pl->rows_few) pl->rows_few = (int)rows;
     }
+    const int sms = sm_count_ext();
+    pl->grid_many *= sms;
+    pl->grid_few = pl->rows_few ? cache_few_grid(sms, pl->rows_few) : 0;
   }
   const size_t part_few = 2 * (size_t)pl->grid_few * cache_few_part_bytes((int)a->cache.dh);
   const size_t part_many = 2 * (size_t)pl->grid_many * cache_many_part_bytes((int)a->cache.dh);
@@ -266,7 +270,7 @@ int rocs_dca_cache_forward(const rocs_dca_cache_args* a, rocs_stream_t stream) {
     p.rows_lo = 0;
     p.rows_hi = pl.rows_hi;
     p.cnt = reinterpret_cast<int*>(ws + sizeof(WsHeader));
-    if (launch_cache_few(p, (int)a->cache.dh, pl.grid_few, st) != cudaSuccess) return ROCS_ERR_CUDA;
+    if (launch_cache_few(p, (int)a->cache.dh, pl.rows_few, pl.grid_few, st) != cudaSuccess) return ROCS_ERR_CUDA;
     ++launches;
   }
   if (pl.grid_many) {
