@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // of an 8 x 8 mat
 }
 
 template <int DH, int NB>
-__global__ void __launch_bounds__(kThreadsFew, NB == 1 ? 5 : 3) rocs_cache_few_kernel(const __grid_constant__ CacheAttnParams p) {
+__global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __grid_constant__ CacheAttnParams p) {
   using L = FewSmem<DH, NB>;
   constexpr int KS = DH / 16;   // contraction steps of Q K^T, and 16-channel tiles of O
   constexpr int CH = DH / 4;    // channels of a row that a lane holds in Q K^T
@@ -425,7 +425,7 @@ cudaError_t launch_few(const CacheAttnParams& p, int grid, cudaStream_t st) {
 
 }  // namespace
 
-int cache_few_grid(int sms, int rows) { return (rows <= 8 ? 5 : 3) * sms; }
+int cache_few_grid(int sms) { return 3 * sms; }
 size_t cache_few_part_bytes(int dh) { return (size_t)(dh == 128 ? few_part<128>() : few_part<64>()) * sizeof(float); }
 
 cudaError_t launch_cache_few(const CacheAttnParams& p, int dh, int rows, int grid, cudaStream_t st) {

@@ -76,7 +76,7 @@ struct CacheAttnParams {
 };
 constexpr int kFewRows = 16;   // rows of a unit of the kernel for few rows, at most
 size_t cache_few_part_bytes(int dh);
-int cache_few_grid(int sms, int rows);  // rows: the most that a key head of a request of this launch has
+int cache_few_grid(int sms);
 struct CacheManyParams {
   CUtensorMap tm_q;          // Q viewed as [tokens][H][dh], box {64, G, 128 / G}
   CacheAttnParams a;
@@ -85,6 +85,7 @@ struct CacheManyParams {
 };
 size_t cache_many_part_bytes(int dh);  // partial results of one unit
 cudaError_t launch_cache_many(const CacheManyParams& p, int dh, int grid, cudaStream_t st);
+// rows: the most that a key head of a request of this launch has
 cudaError_t launch_cache_few(const CacheAttnParams& p, int dh, int rows, int grid, cudaStream_t st);
 
 }  // namespace rocs

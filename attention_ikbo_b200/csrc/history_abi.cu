@@ -218,7 +218,7 @@ int attn_validate(const rocs_dca_cache_args* a, AttnPlan* pl) {
     }
     const int sms = sm_count_ext();
     pl->grid_many *= sms;
-    pl->grid_few = pl->rows_few ? cache_few_grid(sms, pl->rows_few) : 0;
+    pl->grid_few = pl->rows_few ? cache_few_grid(sms) : 0;
   }
   const size_t part_few = 2 * (size_t)pl->grid_few * cache_few_part_bytes((int)a->cache.dh);
   const size_t part_many = 2 * (size_t)pl->grid_many * cache_many_part_bytes((int)a->cache.dh);
