@@ -174,7 +174,13 @@ int cache_move(const rocs_cache_move_args* a, bool append, cudaStream_t st) {
 }
 
 // ---------------------------------------------------------------- attention over the cache
-constexpr int kFewLimit = 32;   // rows of a key head up to which a request goes to the kernel for few rows
+// Which kernel takes which request is chosen by what their units cost, as measured with equal histories (32 of 4096 keys, 8
+// heads): the kernel for few rows takes 59 us (dh = 64: 39) for every 16 rows of the key heads, the one for many 155 (140)
+// for up to 256, so up to 32 (48) rows are better off with the first.  Calls of a single kind get one kernel; calls with
+// both kinds get both kernels, one after the other, only where that saves a fifth, because each ends in a tail of its own
+// (16 requests of 16-64 rows: 37 us with the first alone, 46 with the second alone, 62 with both).
+constexpr int kFewCost = 10, kManyCost128 = 26, kManyCost64 = 36;
+constexpr int kFewLimit128 = 32, kFewLimit64 = 48;
 constexpr int kMaxShared = 64;  // query heads to a key head up to which a 128-row tile is well filled
 inline size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
 
@@ -210,12 +216,26 @@ int attn_validate(const rocs_dca_cache_args* a, AttnPlan* pl) {
     if (a->q_ld != 0 && a->q_ld < row) return ROCS_ERR_INVALID_ARG;
     if (a->q_ld % 8 || a->q_ld >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
     const int64_t G = a->H / a->cache.heads;
-    pl->rows_hi = G > kMaxShared ? 0x7fffffff : kFewLimit;
+    const bool wide = a->cache.dh == 128;
+    const int64_t limit = wide ? kFewLimit128 : kFewLimit64, many = wide ? kManyCost128 : kManyCost64;
+    const int64_t chunk = G > kMaxShared ? 1 : 2 * (128 / G) * G;
+    int64_t all_few = 0, all_many = 0, mixed = 0, most = 0;
     for (int64_t r = 0; r < a->R; ++r) {
       const int64_t rows = (a->cand_off_host[r + 1] - a->cand_off_host[r]) * a->q * G;
-      if (rows > pl->rows_hi) pl->grid_many = 1;
-      else if (rows > pl->rows_few) pl->rows_few = (int)rows;
+      const int64_t f = kFewCost * ((rows + kFewRows - 1) / kFewRows), m = many * ((rows + chunk - 1) / chunk);
+      all_few += f;
+      all_many += m;
+      mixed += rows <= limit ? f : m;
+      if (rows > most) most = rows;
     }
+    if (G > kMaxShared || (all_few <= all_many && 4 * all_few <= 5 * mixed)) pl->rows_hi = 0x7fffffff;
+    else pl->rows_hi = 4 * all_many <= 5 * mixed ? 0 : (int)limit;
+    // the rows that the first kernel sees at most (its unit size goes by them), and whether the second has work
+    for (int64_t r = 0; r < a->R; ++r) {
+      const int64_t rows = (a->cand_off_host[r + 1] - a->cand_off_host[r]) * a->q * G;
+      if (rows <= pl->rows_hi && rows > pl->rows_few) pl->rows_few = (int)rows;
+    }
+    pl->grid_many = most > pl->rows_hi ? 1 : 0;
     const int sms = sm_count_ext();
     pl->grid_many *= sms;
     pl->grid_few = pl->rows_few ? cache_few_grid(sms) : 0;

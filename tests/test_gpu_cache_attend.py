@@ -102,6 +102,10 @@ CASES = [  # counts, q, lens, H, key heads, dh, page, limits
     ([1] * 300, 1, [(7 * i) % 90 for i in range(300)], 2, 1, 64, 16, True),
     ([3] * 40, 2, [1 + 31 * i for i in range(40)], 4, 1, 128, 64, False),
     ([60] * 9, 1, [13 * i for i in range(9)], 7, 1, 128, 32, True),
+    ([1] * 40 + [300, 0, 200], 1, [(11 * i) % 200 for i in range(43)], 2, 2, 128, 64, True),
+    ([3] * 30 + [260] + [2] * 10, 1, [(17 * i) % 150 for i in range(41)], 4, 2, 64, 16, False),
+    ([9, 30, 2], 1, [600, 70, 33], 1, 1, 128, 16, False),
+    ([2, 1], 1, [300, 129], 130, 2, 64, 32, True),
 ]
 
 
