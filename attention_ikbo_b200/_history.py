@@ -154,7 +154,13 @@ def _csr(off, dev, idx, what):
     return d, h, ptr, h.__array_interface__["data"][0], R, int(h[R])
 
 
-def _on(t, what, fn, args, dims=None):
+def _ws(nbytes, dev, idx, given):
+    if given is not None and (given.get_device() != idx or not given.is_contiguous()):
+        raise RocsError(6, "workspace: a contiguous tensor on the call's device")
+    return _workspace(nbytes, dev, given)
+
+
+def _on(t, what, fn, args):
     """``fn(index of t's device, *args)`` with that device current."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise RocsError(1, f"{what} must be a CUDA tensor")
@@ -241,7 +247,7 @@ def _norm_rope(idx, x, q, k, pos_q, pos_k, rope, norm, gamma_q, gamma_k, beta_q,
     dh = x.shape[2]
     sq, q_out = _side(q, q_out, pos_q, gamma_q, beta_q, rope, "q", idx, dtype, dh)
     sk, k_out = _side(k, k_out, pos_k, gamma_k, beta_k, rope, "k", idx, dtype, dh)
-    ws = _workspace(256, x.device, workspace)
+    ws = _ws(256, x.device, idx, workspace)
     _run(_lib().rocs_qk_norm_rope_forward,
          _PACK_NORM.pack(*sq, *sk, dh, _DTYPES[dtype], NORMS[norm] if isinstance(norm, str) else int(norm), eps, *_rope(rope, idx),
                          1 if interleaved else 0, ws.data_ptr(), ws.nbytes), stream, idx, "rocs_qk_norm_rope_forward")
@@ -306,7 +312,7 @@ def _append(idx, cache, k, v, tok_off, base, page_table, rope, pos, interleaved,
     if k.dtype not in _DTYPES:
         raise RocsError(1, "k and v must be bf16 or fp32")
     csr = _csr(tok_off, k.device, idx, "tok_off")
-    ws = _workspace(256, k.device, workspace)
+    ws = _ws(256, k.device, idx, workspace)
     _move(_lib().rocs_cache_append, "rocs_cache_append", idx, _cache(cache, idx), csr, k, v, base, page_table, rope, pos, interleaved,
           k.dtype, ws, stream)
     _hold(stream, ws, csr[0])
@@ -328,7 +334,7 @@ def _read(idx, cache, tok_off, base, page_table, k, v, workspace, stream):
         k = torch.empty((csr[5], c[6], c[7]), dtype=torch.bfloat16, device=dev)
     if v is None:
         v = torch.empty_like(k) if k.is_contiguous() else torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
-    ws = _workspace(256, dev, workspace)
+    ws = _ws(256, dev, idx, workspace)
     _move(_lib().rocs_cache_read, "rocs_cache_read", idx, c, csr, k, v, base, page_table, None, None, False, torch.bfloat16, ws, stream)
     _hold(stream, ws, csr[0], k, v)
     rocs_cache_read.last_workspace = ws
@@ -372,7 +378,7 @@ def _dca_cache(idx, q_t, cache, page_table, seq_len, cand_off, q_tokens, scale, 
     a = (*c, R, int(q_tokens), H, cols, scale, off_d, off_h, _per_request(seq_len, R, "seq_len", idx), table, lim_ptr, q_ptr, q_ld,
          _ptr(o, torch.bfloat16, "o", idx, 3), lse_ptr)
     nbytes = lib.rocs_dca_cache_workspace_size(_PACK_DCA.pack(*a, 0, 0))
-    ws = _workspace(nbytes, q_t.device, workspace)  # 0: refused arguments, the call below says which
+    ws = _ws(nbytes, q_t.device, idx, workspace)  # 0: refused arguments, the call below says which
     _run(lib.rocs_dca_cache_forward, _PACK_DCA.pack(*a, ws.data_ptr(), ws.nbytes), stream, idx, "rocs_dca_cache_forward")
     _hold(stream, ws, off_dev, o, lse)
     rocs_dca_cache_forward.last_workspace = ws

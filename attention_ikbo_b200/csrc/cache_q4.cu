@@ -32,7 +32,14 @@ __device__ __forceinline__ Place places(const CacheMoveParams& p, int t0, int n,
   int r = request_of(p.tok_off, p.R, t0, lane);
   if (lane < n) {
     const int t = t0 + lane;
-    while (r + 1 < p.R && p.tok_off[r + 1] <= t) ++r;
+    if (r + 1 < p.R && p.tok_off[r + 1] <= t) {  // a later request's, perhaps behind many without tokens
+      int hi = p.R;
+      while (hi - r > 1) {
+        const int mid = r + (hi - r) / 2;
+        if (p.tok_off[mid] <= t) r = mid;
+        else hi = mid;
+      }
+    }
     const int64_t slot = (int64_t)p.base[r] + (t - p.tok_off[r]);
     q.slot = (int)slot;
     const int64_t k = slot >> p.c.page_log2;

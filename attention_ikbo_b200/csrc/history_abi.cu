@@ -215,6 +215,14 @@ int attn_validate(const rocs_dca_cache_args* a, AttnPlan* pl) {
     const int64_t row = a->H * a->cache.dh;
     if (a->q_ld != 0 && a->q_ld < row) return ROCS_ERR_INVALID_ARG;
     if (a->q_ld % 8 || a->q_ld >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
+    // outputs that overlap the queries or each other: queries are read again after other parts' outputs are written
+    const int64_t n = pl->C * a->q;
+    const Span q = span(a->q_ptr, n, row, a->q_ld ? a->q_ld : row, 2), o = span(a->o_ptr, n, row, row, 2);
+    if (q.lo < o.hi && o.lo < q.hi) return ROCS_ERR_INVALID_ARG;
+    if (a->lse_ptr) {
+      const Span l = span(a->lse_ptr, n, a->H, a->H, 4);
+      if ((l.lo < q.hi && q.lo < l.hi) || (l.lo < o.hi && o.lo < l.hi)) return ROCS_ERR_INVALID_ARG;
+    }
     const int64_t G = a->H / a->cache.heads;
     const bool wide = a->cache.dh == 128;
     const int64_t limit = wide ? kFewLimit128 : kFewLimit64, many = wide ? kManyCost128 : kManyCost64;

@@ -565,6 +565,9 @@ ROCS_API int rocs_cache_read(const rocs_cache_move_args* args, rocs_stream_t str
  * masked row of the cache holds does not matter; a visible row that is held as NaN makes the result
  * NaN.  scale >= 0 and finite.  A length outside [0, max_pages * page] is cut to that range, a page
  * outside [0, pages) is replaced by page 0, and either sets ROCS_ERR_DEVICE_INDEX.  C*q*H < 2^31.
+ * o_ptr and lse_ptr must not overlap q_ptr's rows or each other.  The kernels (one, or one for
+ * requests with few rows and one for the others) are chosen by cand_off_host: the offsets on the
+ * device must be the same, in replays of a captured call too.
  * The workspace size depends on the current device's SM count. */
 typedef struct {
   rocs_cache_q4 cache;

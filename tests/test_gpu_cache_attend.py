@@ -271,3 +271,87 @@ def test_norm_append_attend_together(ikbo, n):
     kd, vd = ikbo.rocs_cache_read(cache, seq, torch.zeros_like(lens), table)
     od, _ = ikbo.rocs_dca_forward(q, kd, vd, off, seq, 1, dh ** -0.5)
     assert torch.all((od.cpu().double() - ro).abs() <= 2.0 ** -8 * ro.abs() + 2.0 ** -5 * vmax)
+
+
+def test_outputs_over_queries_are_refused(ikbo):
+    s = Setup(ikbo, [3], 1, [40], 2, 2, 64, 16, 21)
+    q = s.q.cuda()
+    with pytest.raises(ikbo.RocsError):
+        s.call(ikbo, q=q, o=q)
+
+
+@pytest.mark.parametrize("n", [4, 300])
+def test_infinite_and_nan_queries_stay_in_their_rows(ikbo, n):
+    s = Setup(ikbo, [n, 2], 1, [260, 40], 2, 1, 64, 32, 22)
+    good = s.call(ikbo)
+    s.q[1, 0, 5] = math.nan
+    s.q[2, 1, 9] = math.inf
+    s.limit = torch.tensor([260] * (n + 2), dtype=torch.int32)
+    s.limit[3] = 0
+    s.q[3] = math.nan  # sees nothing: O = 0, LSE = -inf all the same
+    o, lse = s.call(ikbo)
+    assert torch.isnan(o[1, 0]).all() and torch.isnan(lse[1, 0]) and torch.isnan(o[2, 1]).any()
+    assert torch.all(o[3] == 0) and torch.all(lse[3] == -math.inf)
+    keep = torch.ones(n + 2, 2, dtype=torch.bool)
+    keep[1, 0] = keep[2, 1] = False
+    keep[3] = False
+    # Not the same bits: which maximum a row's sums are taken against depends on its neighbours in the warp (votes, limits).
+    # Each side's LSE is off by at most 260 additions of 2^-24 and 2^-24 of scores below 2^6 (in base 2), each P by one
+    # rounding to bf16, each output by another.
+    assert torch.all((lse.cpu() - good[1].cpu())[keep].abs() <= 2 * (260 + 64 + 16) * 2.0 ** -24)
+    vmax = float(ref.values(s.host[1], s.host[3]).nan_to_num(0.0).abs().max())
+    assert torch.all((o.cpu().float() - good[0].cpu().float())[keep].abs() <= 2 * 2.0 ** -8 * 2 * vmax)
+
+
+def test_two_streams_at_once(ikbo):
+    """Calls on two streams at the same time, each with its own workspace."""
+    a, b = Setup(ikbo, [300, 3], 1, [500, 90], 2, 2, 128, 64, 23), Setup(ikbo, [2, 5], 2, [700, 20], 4, 2, 64, 16, 24)
+    want = a.call(ikbo), b.call(ikbo)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(5):
+        with torch.cuda.stream(sa):
+            x = a.call(ikbo)
+        with torch.cuda.stream(sb):
+            y = b.call(ikbo)
+        got.append((x, y))
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert all(torch.equal(u, w) for u, w in zip(x + y, want[0] + want[1]))
+
+
+def test_scores_that_grow_along_the_history(ikbo):
+    """Every block of keys raises the rows' maxima by far: what was summed before moves to the new maximum each time."""
+    for n in (3, 20, 200):
+        s = Setup(ikbo, [n], 1, [700], 1, 1, 128, 64, 25)
+        k, v, ks, vs = s.host
+        j = torch.arange(700)
+        pg, sl = s.table[0].long()[j // 64], j % 64
+        ks[pg, 0, sl] = ks[pg, 0, sl] * (2.0 ** (j // 70).float())[:, None].bfloat16()
+        o, lse = Setup.call(_moved(ikbo, s), ikbo)
+        s.check(o, lse)
+
+
+def test_long_cache_rows_past_32_bits(ikbo):
+    """A pool whose rows lie past 2^31 codes and 2^32 bytes from its start."""
+    page, heads, dh = 128, 16, 128
+    pages = (1 << 32) // (page * heads * dh // 2) + 40  # 4.3 GB of codes each
+    c = ikbo.CacheQ4(*(torch.zeros(pages, heads, page, dh // 2, dtype=torch.uint8, device="cuda") for _ in range(2)),
+                     *(torch.zeros(pages, heads, page, 2, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(200, heads, dh, generator=g).bfloat16() for _ in range(2))
+    table = torch.tensor([[pages - 1, pages - 30]], dtype=torch.int32).cuda()
+    zero = torch.zeros(1, dtype=torch.int32).cuda()
+    ikbo.rocs_cache_append(c, k.cuda(), v.cuda(), [0, 200], zero, table)
+    kr, vr = ikbo.rocs_cache_read(c, [0, 200], zero, table)
+    small = ikbo.CacheQ4(*(t[[pages - 1, pages - 30]].contiguous() for t in c))
+    t2 = torch.tensor([[0, 1]], dtype=torch.int32).cuda()
+    lens = torch.tensor([200], dtype=torch.int32).cuda()
+    k2, v2 = ikbo.rocs_cache_read(small, [0, 200], zero, t2)
+    assert torch.equal(kr, k2) and torch.equal(vr, v2)
+    for n in (2, 150):
+        q = torch.randn(n, heads, dh, generator=g).bfloat16().cuda()
+        far = ikbo.rocs_dca_cache_forward(q, c, table, lens, [0, n], 1, 0.1)
+        near = ikbo.rocs_dca_cache_forward(q, small, t2, lens, [0, n], 1, 0.1)
+        assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1])

@@ -235,3 +235,45 @@ def test_dense_path_reads_the_cache(ikbo):
     o, lse = ikbo.rocs_dca_forward(q, kr, vr, [0, 3, 5], off, 1, 0.125)
     oo, ll = ref.attend(q, [t.cpu() for t in cache], table, [100, 40], [0, 3, 5], 1, 0.125)
     assert (o.cpu().double() - oo).abs().max() <= 1e-2 * oo.abs().max() + 1e-3
+
+
+def test_tokens_behind_many_empty_requests(ikbo):
+    """Tokens of one warp that belong to requests far apart."""
+    counts = [0] * 5000 + [2] + [0] * 4000 + [3, 0, 1] + [0] * 3000
+    base = [7 * (i % 3) for i in range(len(counts))]
+    k, v, off, b, table, cache = setup(ikbo, counts, base, 16, 2, 64, 5)
+    ikbo.rocs_cache_append(cache, k.cuda(), v.cuda(), off, b.cuda(), table.cuda())
+    assert status(ikbo, ikbo.rocs_cache_append) == (0, 0)
+    pg, sl = places(off, b, table, 16)
+    check_rows(cache.k_codes[pg.cuda(), :, sl.cuda()], cache.k_scale[pg.cuda(), :, sl.cuda()], k.double(), 0)
+    kr, vr = ikbo.rocs_cache_read(cache, off, b.cuda(), table.cuda())
+    assert torch.equal(kr.cpu(), ref.values(cache.k_codes.cpu()[pg, :, sl], cache.k_scale.cpu()[pg, :, sl]).float().bfloat16())
+    assert vr.shape == v.shape
+
+
+def test_quotients_of_exactly_a_half(ikbo):
+    """Values on a grid whose quotients are n + 1/2: half to even, and every code is used."""
+    dh = 128
+    x = torch.empty(40, 2, dh)
+    x[..., 0::2] = torch.arange(dh // 2) % 16           # whole codes 0 ... 15: step 1, minimum 0
+    x[..., 1::2] = (torch.arange(dh // 2) % 15) + 0.5   # halves
+    x = x * torch.tensor([2.0 ** (i - 20) for i in range(40)])[:, None, None]
+    cache = ikbo.CacheQ4.empty(3, 16, 2, dh)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32).cuda()
+    zero = torch.zeros(1, dtype=torch.int32).cuda()
+    for dt in (torch.bfloat16, torch.float32):
+        ikbo.rocs_cache_append(cache, x.to(dt).cuda(), (-x).to(dt).cuda(), [0, 40], zero, table)
+        j = torch.arange(40)
+        pg, sl = table.cpu()[0].long()[j // 16], j % 16
+        c, step, mn = ref.quantise(x.double())
+        assert torch.equal(ref.codes_of(cache.k_codes[pg.cuda(), :, sl.cuda()]), c)
+        assert torch.equal(cache.k_scale[pg.cuda(), :, sl.cuda()].cpu().double(), torch.stack((step, mn), -1))
+        assert torch.equal(ref.codes_of(cache.v_codes[pg.cuda(), :, sl.cuda()]), ref.quantise(-x.double())[0])
+
+
+def test_refused_workspaces(ikbo):
+    x = torch.randn(4, 2, 64, device="cuda").bfloat16()
+    for ws in (torch.empty(256, dtype=torch.uint8), torch.empty(512, dtype=torch.uint8, device="cuda")[::2],
+               torch.empty(100, dtype=torch.uint8, device="cuda"), torch.empty(512, dtype=torch.uint8, device="cuda")[16:]):
+        with pytest.raises(ikbo.RocsError):
+            ikbo.rocs_qk_norm_rope_forward(x, workspace=ws)

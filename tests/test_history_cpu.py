@@ -118,7 +118,7 @@ def test_cache_attention_refusals(lib):
     def args(off=(0, 3, 5), cache=None, **kw):
         off = np.asarray(off, np.int32)
         a = dict(cache=cache or _cache_args(m), R=len(off) - 1, q=1, H=4, max_pages=4, scale=0.1, cand_off_dev=FAKE,
-                 cand_off_host=off.ctypes.data, seq_len=FAKE, page_table=FAKE, q_ptr=FAKE, o_ptr=FAKE, workspace=FAKE,
+                 cand_off_host=off.ctypes.data, seq_len=FAKE, page_table=FAKE, q_ptr=FAKE, o_ptr=FAKE + (1 << 20), workspace=FAKE,
                  workspace_bytes=1 << 40)
         a.update(kw)
         x = m.DcaCacheArgs(**a)
@@ -135,7 +135,9 @@ def test_cache_attention_refusals(lib):
                      ({"seq_len": FAKE + 2}, 1), ({"H": 5}, 1), ({"H": 0}, 1), ({"q": 0}, 1), ({"R": -1}, 1), ({"max_pages": -1}, 1),
                      ({"max_pages": 1 << 26}, 3), ({"q": 1 << 20}, 3), ({"H": 1 << 16}, 3), ({"q": 1 << 19, "H": 1 << 15}, 3),
                      ({"scale": -1.0}, 1), ({"scale": float("nan")}, 1), ({"scale": float("inf")}, 1), ({"q_ld": 64}, 1),
-                     ({"q_ld": 260}, 3), ({"q_ld": 1 << 31}, 3)]:
+                     ({"q_ld": 260}, 3), ({"q_ld": 1 << 31}, 3), ({"o_ptr": FAKE}, 1), ({"o_ptr": FAKE + 2032}, 1),
+                     ({"lse_ptr": FAKE + 64}, 1), ({"lse_ptr": FAKE + (1 << 20) + 2044}, 1),
+                     ({"q_ld": 1 << 18, "o_ptr": FAKE + 1024}, 1)]:
         assert f(P(args(**kw)), None) == code, kw
         assert size(P(args(**kw))) == 0, kw
     need = size(P(args()))
