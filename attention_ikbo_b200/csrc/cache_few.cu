@@ -4,9 +4,11 @@
 //
 // The codes go to the tensor core as they are: 16 + c is exact in bf16 (four mantissa bits under a leading one), so
 //   q_i . k_j = sK_j (q_i . (16 + cK_j)) + (mK_j - 16 sK_j) sum(q_i)
-//   O_i       = sum_j P'_ij (16 + cV_j) - 16 sum_j P'_ij + sum_j p_ij mV_j,     P'_ij = bf16(p_ij sV_j)
-// and unpacking costs a shift and one three-input logic operation for two values.  Scores are exact up to fp32 sums;
-// the one rounding to fewer bits is that of P' (it multiplies codes on the tensor core in bf16).
+//   O_i       = sum_j P'_ij (16 + cV_j) - 16 sum_j P'_ij + sum_j p_ij mV_j,     P'_ij = p_ij sV_j
+// and unpacking costs a shift and one three-input logic operation for two values.  Scores are exact up to fp32 sums.  P'
+// goes to the tensor core in two bf16 parts (16 bits): in one part its rounding, times codes that are not centred as values
+// are, left O three times as far from the exact result as the rounding of the output alone (0.0048 of its norm against
+// 0.0017), and the second product costs little where unpacking is the bound.
 //
 // With a few rows to a pair of (request, key head) each 4-bit value is used a few times: the bytes of the cache and the
 // unpacking bound it.  mma.sync takes its operands from registers, so codes go from shared memory through the logic
@@ -15,7 +17,7 @@
 // where a tcgen05 tile has at least 64: S^T = K Q^T, O^T = V^T P^T, and an 8 x 8 transposition (movmatrix) turns S^T's
 // layout into that of P^T.  NB = 1 or 2 blocks of 8 rows share the unpacked codes.  With query rows as the 16 rows of the
 // instruction (8 keys or channels to each) it issued twice the products and exponentials for up to 8 rows, and took 204
-// us where this takes 154 us (32 histories of 8192-16384 keys, 8 heads of 128, 4 rows).
+// us where this took 144 us with P in one part, and takes 154 us (32 histories of 8192-16384 keys, 8 heads of 128, 4 rows).
 //
 // Each warp takes 16 keys at a time through its own ring of cp.async stages (a 16-key granule never crosses a page) with its
 // own running softmax: no block-wide synchronisation until the unit's end, where the four warps' results are joined in
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
           }
         }
       }
-      uint32_t pb[NB][2];
+      uint32_t pb[NB][2], pl[NB][2];  // high and low parts
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float mu[2] = {m[b][0] == -INFINITY ? 0.0f : m[b][0], m[b][1] == -INFINITY ? 0.0f : m[b][1]};
@@ -269,9 +271,11 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
             if (key0 + g + 8 * h >= lim[b][1]) w1 = c1 = 0.0f;
           }
           const uint32_t pk = pack_bf16x2(w0, w1);
-          corr[b][0] += fmaf(-16.0f, bf_lo(pk), c0);
-          corr[b][1] += fmaf(-16.0f, bf_hi(pk), c1);
+          // what the two parts leave of P' is below 2^-17 of it: the sum of P' is taken as it is
+          corr[b][0] += fmaf(-16.0f, w0, c0);
+          corr[b][1] += fmaf(-16.0f, w1, c1);
           pb[b][h] = transpose8(pk);
+          pl[b][h] = transpose8(pack_bf16x2(w0 - bf_lo(pk), w1 - bf_hi(pk)));
         }
       }
       // P V: keys 2t, 2t + 1 of both halves; this lane's DH/8 channels of each
@@ -302,6 +306,10 @@ __global__ void __launch_bounds__(kThreadsFew, 3) rocs_cache_few_kernel(const __
           mma16816(o[b][4 * k + 1], a1, pb[b][0], pb[b][1]);
           mma16816(o[b][4 * k + 2], a2, pb[b][0], pb[b][1]);
           mma16816(o[b][4 * k + 3], a3, pb[b][0], pb[b][1]);
+          mma16816(o[b][4 * k + 0], a0, pl[b][0], pl[b][1]);
+          mma16816(o[b][4 * k + 1], a1, pl[b][0], pl[b][1]);
+          mma16816(o[b][4 * k + 2], a2, pl[b][0], pl[b][1]);
+          mma16816(o[b][4 * k + 3], a3, pl[b][0], pl[b][1]);
         }
       }
     }

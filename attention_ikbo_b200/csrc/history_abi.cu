@@ -175,11 +175,11 @@ int cache_move(const rocs_cache_move_args* a, bool append, cudaStream_t st) {
 
 // ---------------------------------------------------------------- attention over the cache
 // Which kernel takes which request is chosen by what their units cost, as measured with equal histories (32 of 4096 keys, 8
-// heads): the kernel for few rows takes 59 us (dh = 64: 39) for every 16 rows of the key heads, the one for many 155 (140)
-// for up to 256, so up to 32 (48) rows are better off with the first.  Calls of a single kind get one kernel; calls with
+// heads): the kernel for few rows takes 66 us (dh = 64: 41) for every 16 rows of the key heads, the one for many 155 (140)
+// for up to 256, so up to 32 (48) rows are as well off with the first.  Calls of a single kind get one kernel; calls with
 // both kinds get both kernels, one after the other, only where that saves a fifth, because each ends in a tail of its own
-// (16 requests of 16-64 rows: 37 us with the first alone, 46 with the second alone, 62 with both).
-constexpr int kFewCost = 10, kManyCost128 = 26, kManyCost64 = 36;
+// (16 requests of 16-64 rows of 64: 35 us with the first alone, 46 with the second alone, 62 with both).
+constexpr int kFewCost = 10, kManyCost128 = 24, kManyCost64 = 34;
 constexpr int kFewLimit128 = 32, kFewLimit64 = 48;
 constexpr int kMaxShared = 64;  // query heads to a key head up to which a 128-row tile is well filled
 inline size_t a256(size_t n) { return (n + 255) & ~size_t(255); }
