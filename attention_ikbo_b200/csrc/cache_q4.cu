@@ -11,7 +11,7 @@
 // Each value is read once and leaves as 4 bits; a row's statistics are min and max over its dh/16 lanes.  The places of the
 // (at most 32) tokens are looked up once for the warp, a token to a lane.  The step is rounded to bf16 BEFORE the codes are
 // taken, so that codes are nearest to what they will stand for.  Memory bounds both directions; with one token to a warp and
-// a division for every value the two together took 129 us where they take 84 us (8 histories of 4096-8192 events, 4 heads of
+// a division for every value the two together took 129 us where they take 78 us (8 histories of 4096-8192 events, 4 heads of
 // 128).
 #include "history.cuh"
 

@@ -7,9 +7,9 @@
 //
 // One pass: each value is read and written once, so memory bounds it.  A warp takes U * 512/dh rows (heads of tokens, in
 // their order); the loads of all of them are in flight before the first is used, and values stay packed as they came
-// until their row's turn, so that enough warps fit an SM.  Statistics and rotation in fp32, one rounding when stored.
+// until their row's turn, so that 24 warps fit an SM.  Statistics and rotation in fp32, one rounding when stored.
 // With 8 channels to a lane (half the rows to a warp, partners of a pair 8 lanes apart, one token to a warp) it took 131 us
-// where this takes 78 us (16384 x 8 query and 65536 x 8 key rows of 128, bf16).
+// where this takes 74 us (16384 x 8 query and 65536 x 8 key rows of 128, bf16).
 #include "history.cuh"
 
 namespace rocs {
@@ -17,10 +17,10 @@ namespace rocs {
 namespace {
 
 template <int DH, typename T, int U>
-__global__ void __launch_bounds__(256, 3) rocs_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(128, 6) rocs_norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = DH / 16, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31;
-  int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (w >= p.warps) return;
   const int which = w >= p.warps0;
   const NormRopeSide& sd = p.side[which];
@@ -134,9 +134,9 @@ __global__ void rocs_rope_table_kernel(float* table, int64_t n, int half, double
 
 template <int DH, typename T>
 cudaError_t launch_nr(const NormRopeParams& p, int unroll, cudaStream_t st) {
-  const unsigned grid = (unsigned)((p.warps + 7) / 8);
-  if (unroll == 2) rocs_norm_rope_kernel<DH, T, 2><<<grid, 256, 0, st>>>(p);
-  else rocs_norm_rope_kernel<DH, T, 1><<<grid, 256, 0, st>>>(p);
+  const unsigned grid = (unsigned)((p.warps + 3) / 4);
+  if (unroll == 2) rocs_norm_rope_kernel<DH, T, 2><<<grid, 128, 0, st>>>(p);
+  else rocs_norm_rope_kernel<DH, T, 1><<<grid, 128, 0, st>>>(p);
   return cudaGetLastError();
 }
 
