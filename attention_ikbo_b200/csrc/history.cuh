@@ -15,7 +15,7 @@ __device__ __forceinline__ void load8(const float* p, float* v) {
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-// two fp32 values at once; each product and sum is rounded as the single one is
+// two fp32 values at once (a product and a sum of it may be fused, see Rotation)
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -79,12 +79,14 @@ struct Rotation {
       }
       return;
     }
-    const uint64_t minus = pack2(-1.0f, -1.0f);  // times -1, added: the difference, rounded once
+    // Both results add a product that was taken times -1: the assembler makes one fused operation of a packed product and
+    // a packed sum, whatever their rounding says, but leaves this form alone (a test compares the bits).
+    const uint64_t minus = pack2(-1.0f, -1.0f);
 #pragma unroll
     for (int k = 0; k < 8; k += 2) {
       const uint64_t a = pack2(v[k], v[k + 1]), b = pack2(v[8 + k], v[9 + k]), cc = pack2(c[k], c[k + 1]), ss = pack2(s[k], s[k + 1]);
       unpack2(fma2(mul2(b, ss), minus, mul2(a, cc)), v[k], v[k + 1]);
-      unpack2(add2(mul2(b, cc), mul2(a, ss)), v[8 + k], v[9 + k]);
+      unpack2(fma2(mul2(a, pack2(-s[k], -s[k + 1])), minus, mul2(b, cc)), v[8 + k], v[9 + k]);
     }
   }
 };

@@ -496,6 +496,7 @@ ROCS_API int rocs_rope_table(float* table, int64_t max_pos, int64_t rot, double 
  * One row (a head of a token) holds dh codes c in 0..15 with its step and minimum (in this order) and
  * stands for minimum + step * c, where
  *   minimum = bf16(min x),  step = bf16((max x - min x) / 15),  c = clamp(rint((x - minimum) / step), 0, 15).
+ * (all in fp32; the fifteenth is taken by the reciprocal of 15, the quotient as the division rounds it)
  * In each little-endian 32-bit word of codes (8 channels) nibble i of the low half is channel 2i,
  * nibble i of the high half channel 2i + 1.  A row with an infinity or a NaN in it, or whose range
  * passes fp32, is held with a NaN step and minimum and reads as NaN.

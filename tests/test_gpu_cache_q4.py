@@ -277,3 +277,30 @@ def test_refused_workspaces(ikbo):
                torch.empty(100, dtype=torch.uint8, device="cuda"), torch.empty(512, dtype=torch.uint8, device="cuda")[16:]):
         with pytest.raises(ikbo.RocsError):
             ikbo.rocs_qk_norm_rope_forward(x, workspace=ws)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_codes_of_rotated_keys_are_the_definitions(ikbo, dt, inter):
+    """Codes, steps and minima of rotated keys, bit for bit: rotation in fp32 with every operation rounded, then the format
+    by fp32 division."""
+    dh, heads, T = 128, 4, 4000
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k = (torch.randn(T, heads, dh, generator=g, device="cuda") * 1.7).to(dt)
+    rope = ikbo.rocs_rope_table(T, dh)
+    cache = ikbo.CacheQ4.empty(T // 16, 16, heads, dh)
+    table = torch.arange(T // 16, dtype=torch.int32, device="cuda")[None]
+    ikbo.rocs_cache_append(cache, k, k, [0, T], torch.zeros(1, dtype=torch.int32, device="cuda"), table, rope=rope, interleaved=inter)
+    c, s = rope[:, None, :dh // 2], rope[:, None, dh // 2:]
+    x = k.float()
+    a, b = (x[..., 0::2], x[..., 1::2]) if inter else (x[..., :dh // 2], x[..., dh // 2:])
+    u, v = a * c - b * s, b * c + a * s
+    rotated = torch.stack((u, v), -1).flatten(-2) if inter else torch.cat((u, v), -1)
+    for codes, scale, y in ((cache.k_codes, cache.k_scale, rotated), (cache.v_codes, cache.v_scale, x)):
+        lo, hi = y.amin(-1), y.amax(-1)
+        step, mn = ((hi - lo) / 15).bfloat16(), lo.bfloat16()
+        want = ((y - mn.float()[..., None]) / step.float()[..., None]).round().clamp(0, 15)
+        got = codes.transpose(1, 2).reshape(T, heads, dh // 2)
+        sc = scale.transpose(1, 2).reshape(T, heads, 2)
+        assert torch.equal(sc[..., 0], step) and torch.equal(sc[..., 1], mn)
+        assert torch.equal(ref.codes_of(got), want.cpu().long())

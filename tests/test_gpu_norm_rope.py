@@ -161,3 +161,21 @@ def test_graph_and_other_stream(ikbo):
     want, _ = ikbo.rocs_qk_norm_rope_forward(x, None, pos, None, table)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dh,rot", [(128, 128), (128, 64), (64, 64), (64, 32)])
+def test_rotation_rounds_products_and_sums_one_by_one(ikbo, dh, rot, inter):
+    """The bits of a * c - b * s and b * c + a * s with every operation rounded: what 4-bit codes are taken from must not
+    depend on how the expression was compiled."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(3000, 3, dh, generator=g, device="cuda")
+    pos = torch.randint(0, 4000, (3000,), generator=g, device="cuda", dtype=torch.int32)
+    rope = ikbo.rocs_rope_table(4000, rot)
+    y, _ = ikbo.rocs_qk_norm_rope_forward(x, pos_q=pos, rope=rope, norm="none", interleaved=inter)
+    cs = rope[pos.long()][:, None]
+    c, s = cs[..., :rot // 2], cs[..., rot // 2:]
+    pick = (lambda t: (t[..., 0:rot:2], t[..., 1:rot:2])) if inter else (lambda t: (t[..., :rot // 2], t[..., rot // 2:rot]))
+    a, b = pick(x)
+    u, v = pick(y)
+    assert torch.equal(u, a * c - b * s) and torch.equal(v, b * c + a * s) and torch.equal(y[..., rot:], x[..., rot:])
