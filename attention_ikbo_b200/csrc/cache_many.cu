@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
     for (int k = 0; k < kRecs; ++k) {
       mbar_init(&rec_full[k], 1);
       mbar_init(&rec_empty[k], 1 + 1 + 4 + 8);  // query tiles, issuer, conversion warps, softmax warps
-      mbar_init(&rec_v[k], 4);
+      mbar_init(&rec_v[k], 4);  // conversion warps
     }
     for (int k = 0; k < L::kStaged; ++k) {
       mbar_init(&st_full[k], 1);
@@ -411,7 +411,11 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
       if (!r) break;
       const int step = r->step, n = r->n, keys = r->L, rec = ri, nx = r->row0 + tile_rows < r->rows ? 2 : 1;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&rec_empty[ri]);
+      if (lane == 0) {
+        // every use of a record turns rec_v's phase, for a unit without keys too: its readers count uses of the record
+        if (keys == 0) mbar_arrive(&rec_v[ri]);
+        mbar_arrive(&rec_empty[ri]);
+      }
       rec_step();
       if (keys == 0) continue;
       for (int i = 0; i < 2 * n; ++i) {

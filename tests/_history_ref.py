@@ -114,3 +114,47 @@ def attend(q, cache, table, lens, cand_off, q_tokens, scale, limit=None):
         o[a:b] = pv / torch.where(l == 0, 1.0, l)
         lse[a:b] = (m + torch.log(l))[..., 0]
     return o, lse
+
+
+def attend_rows(q, cache, table, lens, cand_off, q_tokens, scale, limit=None):
+    """:func:`attend` on the device of ``q`` and ``cache`` (64 bits), request by request, with each row's own sums:
+    (o, lse, mag, spread) with mag = sum_j p_j (|v_j| + |minimum_j|) and spread = sqrt(sum_j (p_j v_j)^2), [C*q, H, dh] each.
+    A masked key counts for nothing, a visible row that is held as NaN makes o (keys: lse too) NaN."""
+    k_codes, v_codes, k_scale, v_scale = cache
+    dev, hk, page, dh = q.device, k_codes.shape[1], k_codes.shape[2], 2 * k_codes.shape[3]
+    H = q.shape[1]
+    shift = channel_shift(dh).to(dev)
+
+    def rows(codes, scales, at, within):
+        b = codes[at, :, within].long()
+        w = (b[..., 0::4] | b[..., 1::4] << 8 | b[..., 2::4] << 16 | b[..., 3::4] << 24).repeat_interleave(8, -1)
+        s = scales[at, :, within].double()
+        return (s[..., 1:] + s[..., :1] * (w >> shift & 15).double()).transpose(0, 1), s[..., 1].abs().transpose(0, 1)
+
+    o, mag, spread = (torch.zeros(q.shape, dtype=torch.float64, device=dev) for _ in range(3))
+    lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device=dev)
+    for r in range(len(cand_off) - 1):
+        a, b, n = int(cand_off[r]) * q_tokens, int(cand_off[r + 1]) * q_tokens, int(lens[r])
+        if a == b or n == 0:
+            continue
+        j = torch.arange(n, device=dev)
+        at, within = table[r].to(dev).long()[j // page], j % page
+        k, _ = rows(k_codes, k_scale, at, within)  # [hk, n, dh]
+        v, mn = rows(v_codes, v_scale, at, within)
+        s = q[a:b].double().view(b - a, hk, H // hk, dh).permute(1, 2, 0, 3).reshape(hk, -1, dh) @ k.transpose(1, 2) * scale
+        if limit is not None:
+            lim = limit[a // q_tokens:b // q_tokens].long().repeat_interleave(q_tokens).repeat(H // hk)
+            s = s.masked_fill(j >= lim[:, None], -math.inf)
+        m = s.amax(-1, keepdim=True)
+        p = torch.exp(s - torch.where(m == -math.inf, 0.0, m))
+        l = p.sum(-1, keepdim=True)
+        p = p / torch.where(l == 0, 1.0, l)
+        bad = torch.isnan(v).any(-1)  # [hk, n]
+        seen = (s > -math.inf).double() @ bad.double()[..., None] > 0
+        clean, least = v.masked_fill(bad[..., None], 0.0), mn.masked_fill(bad, 0.0)
+        back = lambda t: t.view(hk, H // hk, b - a, -1).permute(2, 0, 1, 3).reshape(b - a, H, -1)  # noqa: E731
+        o[a:b] = back((p @ clean).masked_fill(seen, math.nan))
+        mag[a:b] = back(p @ (clean.abs() + least[..., None]))
+        spread[a:b] = back(((p * p) @ (clean * clean)).sqrt())
+        lse[a:b] = back(m + l.log())[..., 0]
+    return o, lse, mag, spread
