@@ -14,6 +14,10 @@
 //     of 4096-8192 keys, 4 heads, 8192 rows each); rounding the keys to bf16 would put 2^-9 of every product into the
 //     scores.
 //   * V is rounded to bf16 once, as P is and as the output is: its error is a weighted mean of such roundings.
+//   * The tensor core cuts off what falls below its accumulator, always towards zero: with values of one sign O lost 0.0004
+//     of itself in 131,072 keys and 0.008 in 2,000,000.  So a run over more than kWindow blocks of a unit goes through the
+//     roles in windows, each with an O of its own, joined in fp32 in memory (the place of the run's partial result): 868 ->
+//     874 us for the case above, whose runs have one window.  Windows made in the softmax loop itself took 905 us there.
 // Warp roles (512 threads): warp 0 loads query tiles by TMA, warp 1 issues tcgen05.mma, warp 2 walks the work and copies
 // codes, steps and minima into staging buffers (cp.async.bulk, one copy for each page), warps 4-7 and 8-11 are the
 // softmax and the epilogue of query tiles A and B (S in TMEM; P in bf16 over S, the A operand of P V; O in TMEM), warps
@@ -37,17 +41,20 @@ namespace {
 constexpr int kThreadsMany = 512, BM = 128, BN = 128;
 constexpr int kSoftWarp = 4, kDeqWarp = 12;
 constexpr int kRecs = 4;  // records of units on their way through the roles
+constexpr int kWindow = 256;  // blocks of keys of a record, at most
 // 4 warpgroups launched at 128 registers a thread; the shares add up to what was launched
 constexpr uint32_t kLaunchRegs = 128, kRegsCtl = 64, kRegsDeq = 64, kRegsSoft = 192;
 static_assert(kRegsCtl + kRegsDeq + 2 * kRegsSoft == 4 * kLaunchRegs, "register split");
 
-// One unit's run of key blocks, as warp 2 hands it to the other roles.
+// One unit's run of key blocks, or a window of it, as warp 2 hands it to the other roles.
 struct Rec {
   int c0, rows, L, head;  // first candidate, query rows of the key head, keys of the history, key head
   int row0, step, n;      // first row of tile A, first block of 128 keys, blocks (-1: no more units)
   int cta0, cta1;         // CTAs whose runs hold blocks of the unit
   int bad;                // first key whose V is not finite
-  int pad[6];
+  int slot;               // place of the run's partial result: 1 for a unit's first part, 0 otherwise
+  int window;             // 1: a window of the run came before, + 2: another comes behind
+  int pad[4];
 };
 
 template <int DH>
@@ -114,6 +121,36 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+
+// A window's O (32 rows of a tile in TMEM), maxima and sums joined with those of the run's earlier windows, which stand in
+// memory.  A function of its own, out of the softmax warps' way: inlined it slowed their loop by 4 % though it never ran.
+template <int DH>
+__device__ __noinline__ float2 join_window(uint32_t o_addr, const float* kept, float m, float l) {
+  const int lane = threadIdx.x & 31;
+  const float was_m = __ldcg(kept + DH * 32 + lane), m_new = fmaxf(was_m, m);
+  float was_f = 0.0f, f = 1.0f;  // no key in either: sums of zero (or NaN, which stay)
+  if (m_new > -INFINITY) {
+    was_f = ex2(was_m - m_new);
+    f = ex2(m - m_new);
+  }
+#pragma unroll 1
+  for (int cc = 0; cc < DH / 16; ++cc) {
+    uint32_t ov[16];
+    tmem_ld16(o_addr + cc * 16, ov);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 was = __ldcg(reinterpret_cast<const float4*>(kept + ((cc * 4 + k) * 32 + lane) * 4));
+      ov[4 * k] = __float_as_uint(fmaf(was.x, was_f, __uint_as_float(ov[4 * k]) * f));
+      ov[4 * k + 1] = __float_as_uint(fmaf(was.y, was_f, __uint_as_float(ov[4 * k + 1]) * f));
+      ov[4 * k + 2] = __float_as_uint(fmaf(was.z, was_f, __uint_as_float(ov[4 * k + 2]) * f));
+      ov[4 * k + 3] = __float_as_uint(fmaf(was.w, was_f, __uint_as_float(ov[4 * k + 3]) * f));
+    }
+    tmem_st16(o_addr + cc * 16, ov);
+  }
+  tmem_st_wait();
+  return make_float2(m_new, fmaf(__ldcg(kept + DH * 32 + 32 + lane), was_f, l * f));
 }
 
 }  // namespace
@@ -245,9 +282,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
       const uint32_t code_bytes = page * (DH / 2), scale_bytes = page * 4;
       const uint32_t staging = smem_u32(smem + L::off_staging);
       bool ok = true;
-      for (bool more = true; more && ok; more = w.next(p)) {
+      int from = 0;  // blocks of the run that earlier windows have taken
+      for (bool more = true; more && ok;) {
         if (!(ok = mbar_wait_sleep<200>(&rec_empty[ri], rec_ph ^ 1, ctl, 952))) break;
-        const int n = w.count(), keys = w.q.L;
+        const int left = w.count() - from, n = min(left, kWindow), first = w.step + from, keys = w.q.L;
         if (lane == 0) {
           volatile Rec& r = recs[ri];
           r.c0 = w.q.c0;
@@ -255,23 +293,24 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
           r.L = keys;
           r.head = w.head;
           r.row0 = w.chunk * 2 * tile_rows;
-          r.step = w.step;
+          r.step = first;
           r.n = n;
           r.cta0 = w.first_cta();
           r.cta1 = w.last_cta();
           r.bad = 0x7fffffff;
+          r.slot = w.step == 0 ? 1 : 0;
+          r.window = (from > 0 ? 1 : 0) | (n < left ? 2 : 0);
           mbar_arrive(&rec_full[ri]);
         }
         rec_step();
-        if (keys == 0) continue;
         const int32_t* table = p.table + (int64_t)w.r * p.max_pages;
         auto page_at = [&](int j) {
-          const int key = (w.step + j) * BN + (int)lane * 16;
+          const int key = (first + j) * BN + (int)lane * 16;
           return j < n && mine && key < keys ? table[key >> p.c.page_log2] : 0;
         };
         auto copy = [&](int kv, int j, int pg) -> bool {
           if (!mbar_wait_sleep<200>(&st_empty[si], sph ^ 1, ctl, 953)) return false;
-          const int key = (w.step + j) * BN + (int)lane * 16;
+          const int key = (first + j) * BN + (int)lane * 16;
           const bool go = mine && key < keys;
           if (go && (unsigned)pg >= (unsigned)p.c.pages) {
             record_error(p.ws, ROCS_ERR_DEVICE_INDEX, 951);
@@ -292,13 +331,18 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         };
         // blocks in the order of their use: K0, K1, V0, K2, V1, ..., V_last
         int now = 0, next = page_at(0);
-        for (int j = 0; j < n && ok; ++j) {
+        for (int j = 0; j < n && keys > 0 && ok; ++j) {
           const int before = now;
           now = next;
           next = page_at(j + 1);
           ok = copy(0, j, now) && (j == 0 || copy(1, j - 1, before));
         }
-        if (ok) ok = copy(1, n - 1, now);
+        if (ok && keys > 0) ok = copy(1, n - 1, now);
+        from += n;
+        if (n == left) {
+          from = 0;
+          more = w.next(p);
+        }
       }
       if (ok && mbar_wait_sleep<200>(&rec_empty[ri], rec_ph ^ 1, ctl, 954) && lane == 0) {
         recs[ri].n = -1;
@@ -694,12 +738,18 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
       tc_fence_after();
 
       // A unit cut by the border of a run: each part leaves its unnormalised O, maxima and sums and counts itself in;
-      // the last one (it waits for nobody) merges all parts in their order.
+      // the last one (it waits for nobody) merges all parts in their order.  Windows of a run are joined in the same place
+      // one by one; a unit that is not cut takes that of a unit's first part, which only the CTA's last unit needs, later.
       const int cta0 = r->cta0, cta1 = r->cta1, slab = x * 4 + quarter;
       const float* parts = nullptr;
-      if (cta0 != cta1) {
+      if (cta0 != cta1 || r->window) {
         constexpr int kSlab = many_slab<DH>();
-        float* mine = p.part + (((int64_t)blockIdx.x * 2 + (step == 0 ? 1 : 0)) * 8 + slab) * kSlab;
+        float* mine = p.part + (((int64_t)blockIdx.x * 2 + r->slot) * 8 + slab) * kSlab;
+        if (r->window & 1) {
+          const float2 ml = join_window<DH>(o_addr, mine, m_used, l);
+          m_used = ml.x;
+          l = ml.y;
+        }
 #pragma unroll 1
         for (int cc = 0; cc < DH / 32; ++cc) {  // [column/4][row][4]: each store a contiguous 512 bytes
           uint32_t ov[32];
@@ -717,9 +767,11 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
         __stcg(mine + DH * 32 + 32 + lane, l);
         __threadfence();
         __syncwarp();
-        int order = 0;
-        if (lane == 0) order = atomicAdd(&p.cnt[cta0 * 8 + slab], 1);
-        order = __shfl_sync(0xffffffffu, order, 0);
+        int order = r->window & 2 ? -1 : 0;
+        if (order == 0 && cta0 != cta1) {
+          if (lane == 0) order = atomicAdd(&p.cnt[cta0 * 8 + slab], 1);
+          order = __shfl_sync(0xffffffffu, order, 0);
+        }
         if (order != cta1 - cta0) {
           tc_fence_before();
           __syncwarp();

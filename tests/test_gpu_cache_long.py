@@ -52,6 +52,7 @@ CASES = [  # keys, requests, candidates, key heads, heads to each, dh, offset of
     (131072, 64, 4, 8, 1, 128, 3.0),
     (131072, 8, 300, 8, 1, 128, 0.0),
     (262144, 6, 300, 8, 1, 64, 3.0),
+    (600000, 40, 300, 2, 1, 64, 3.0),
 ]
 
 
@@ -77,22 +78,23 @@ def test_error_does_not_grow_with_the_history(ikbo, n, R, cand, hk, G, dh, offse
         assert torch.all(err.norm(dim=-1) <= (2.0 ** -8 + 2.0 ** -12) * ro.norm(dim=-1))
 
 
-@pytest.mark.parametrize("cand,G,dh", [(2, 1, 128), (3, 4, 64)])
-def test_maxima_and_limits_over_a_long_run(ikbo, cand, G, dh):
+@pytest.mark.parametrize("n,R,cand,G,dh", [(20000, 300, 2, 1, 128), (20000, 300, 3, 4, 64), (100000, 110, 70, 1, 128),
+                                           (70001, 150, 150, 2, 64)])
+def test_maxima_and_limits_over_a_long_run(ikbo, n, R, cand, G, dh):
     """Runs long enough that sums are joined several times on the way: scores that grow along the history, limits that end
     anywhere (rows that see nothing, or nothing of what comes later), a NaN row behind most limits."""
     from test_gpu_cache_units import check_rows
 
-    n, R, page = 20000, 300, 64
+    page, bad = 64, n * 3 // 5
     cache, one = shared_history(n, 1, dh, page, 0.5, 9)
     j = torch.arange(n, device="cuda")
-    cache[2][j // page, 0, j % page] *= (2.0 ** (j // 2500))[:, None].bfloat16()
-    cache[3][12000 // page, 0, 12000 % page] = math.nan
+    cache[2][j // page, 0, j % page] *= (2.0 ** (j // (n // 8)))[:, None].bfloat16()
+    cache[3][bad // page, 0, bad % page] = math.nan
     g = torch.Generator().manual_seed(6)
     q = (0.05 * torch.randn(R * cand, G, dh, generator=g)).bfloat16().cuda()
     limit = torch.randint(0, n + 1, (R * cand,), generator=g, dtype=torch.int32)
     limit[::7] = torch.randint(0, 70, (len(limit[::7]),), generator=g, dtype=torch.int32)
-    limit[3], limit[4], limit[5], limit[9] = 0, n, 12000, 12001
+    limit[3], limit[4], limit[5], limit[9] = 0, n, bad, bad + 1
     off, lens = [cand * r for r in range(R + 1)], [n - 17 * r for r in range(R)]
     table = one.repeat(R, 1)
     o, lse = ikbo.rocs_dca_cache_forward(q, ikbo.CacheQ4(*cache), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), off, 1,
