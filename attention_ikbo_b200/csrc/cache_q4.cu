@@ -1,8 +1,8 @@
 // cache_q4.cu -- append to and read from the paged 4-bit cache of request histories.
 //
 // A row (one head of one token) of dh values x is held as
-//   minimum = bf16(min x),  step = bf16((max x - min x) / 15),  code = clamp(rint((x - minimum) / step), 0, 15)
-// and stands for  minimum + step * code.  In every 32-bit word of codes (8 channels) nibble i of the low half is
+//   minimum = bf16(min x),  step = bf16((max x - min x) * (1/15)),  code = clamp(rint((x - minimum) / step), 0, 15)
+// in fp32, and stands for  minimum + step * code.  In every 32-bit word of codes (8 channels) nibble i of the low half is
 // channel 2i and nibble i of the high half channel 2i + 1, so that one mask picks a pair of neighbouring channels out
 // of a word, each in its own half.  A row that holds an infinity or a NaN, or whose range passes fp32, is held with a
 // NaN step and minimum: all of it reads as NaN.
@@ -70,8 +70,8 @@ __device__ __forceinline__ void row_min_max(const float (&v)[16], float& lo, flo
 }
 
 // Codes of 8 values, packed: rint((x - mn) / step), held to 0 ... 15 where CLAMP.  The quotient by the reciprocal is
-// corrected with its own remainder (exact, a fused multiply-add), which rounds it as the division does; bf16 values lie on a
-// grid, so quotients of exactly a half are common and have to come out as such.
+// corrected with its own remainder (exact, a fused multiply-add), which rounds it as the division does (Markstein's
+// method); bf16 values lie on a grid, so quotients of exactly a half are common and have to come out as such.
 template <bool CLAMP>
 __device__ __forceinline__ uint32_t codes8(const float* v, float mn, float step, float inv) {
   const uint64_t mn2 = pack2(-mn, -mn), step2 = pack2(-step, -step), inv2 = pack2(inv, inv);
@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(256, 4) rocs_cache_append_kernel(const __grid_
     const float range = hi - lo;
     const unsigned mine = ((1u << LPR) - 1) << (lane & ~(LPR - 1));
     const bool finite = range < INFINITY && !(any & mine);  // false too where range is NaN
-    // a fifteenth by its fp32 reciprocal: off by one unit of fp32 at most, before the rounding to bf16
+    // The format takes a fifteenth by the product: off by one unit of fp32 at most, so that only quotients midway between two
+    // bf16 values may round to the other one, which is as near.
     const __nv_bfloat162 sc = __floats2bfloat162_rn(finite ? range * (1.0f / 15.0f) : NAN, finite ? lo : NAN);
     const float step = __low2float(sc), mn = __high2float(sc);
     uint32_t w0 = 0, w1 = 0;

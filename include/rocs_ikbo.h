@@ -495,8 +495,10 @@ ROCS_API int rocs_rope_table(float* table, int64_t max_pos, int64_t rot, double 
  *   k_codes, v_codes [pages, heads, page, dh/2] bytes     k_scale, v_scale [pages, heads, page, 2] bf16
  * One row (a head of a token) holds dh codes c in 0..15 with its step and minimum (in this order) and
  * stands for minimum + step * c, where
- *   minimum = bf16(min x),  step = bf16((max x - min x) / 15),  c = clamp(rint((x - minimum) / step), 0, 15).
- * (all in fp32; the fifteenth is taken by the reciprocal of 15, the quotient as the division rounds it)
+ *   minimum = bf16(min x),  step = bf16((max x - min x) * (1/15)),  c = clamp(rint((x - minimum) / step), 0, 15).
+ * All in fp32, each operation rounded; 1/15 is the fp32 value nearest to it.  The product differs from the
+ * division by 15 by one unit of fp32 at most, so a step differs only where the quotient lies midway between
+ * two bf16 values: it then is either of them (294, not 292, for a range of 4395).
  * In each little-endian 32-bit word of codes (8 channels) nibble i of the low half is channel 2i,
  * nibble i of the high half channel 2i + 1.  A row with an infinity or a NaN in it, or whose range
  * passes fp32, is held with a NaN step and minimum and reads as NaN.
