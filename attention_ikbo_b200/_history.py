@@ -1,4 +1,8 @@
-"""ctypes marshalling of the history-cache entry points (see ``include/rocs_ikbo.h`` for the contract)."""
+"""ctypes marshalling of the history-cache entry points (see ``include/rocs_ikbo.h`` for the contract).
+
+With ``stream`` a call runs there instead of on the current stream.  The tensors that it is given must be ready on that
+stream (the caller orders the two); what it makes itself comes from that stream's memory and may be used on both.
+"""
 from __future__ import annotations
 
 import ctypes
@@ -91,12 +95,14 @@ class CacheQ4(NamedTuple):
 
 
 def _hold(stream, *tensors):
-    """Tensors made on the current stream and used on another: their memory is not handed out again before that stream
-    has passed this point."""
+    """Tensors that the current stream and the call's may both use: their memory is not handed out again before both have
+    passed this point."""
     if stream is not None:
+        here = torch.cuda.current_stream(stream.device)
         for t in tensors:
             if t is not None and t.is_cuda:
                 t.record_stream(stream)
+                t.record_stream(here)
 
 
 def _refuse(t, dtype, what, idx, dims, contiguous=True):
@@ -154,8 +160,10 @@ def _csr(off, dev, idx, what):
     return d, h, ptr, h.__array_interface__["data"][0], R, int(h[R])
 
 
-def _ws(nbytes, dev, idx, given):
-    if given is not None and (given.get_device() != idx or not given.is_contiguous()):
+def _ws(nbytes, dev, idx, given, stream):
+    if given is None:
+        return _empty(stream, max(int(nbytes), 256), torch.uint8, dev)
+    if given.get_device() != idx or not given.is_contiguous():
         raise RocsError(6, "workspace: a contiguous tensor on the call's device")
     return _workspace(nbytes, dev, given)
 
@@ -169,6 +177,15 @@ def _on(t, what, fn, args):
         return fn(idx, *args)
     with torch.cuda.device(idx):
         return fn(idx, *args)
+
+
+def _empty(stream, shape, dtype, device):
+    """Memory for a call on ``stream``: from that stream's pool, since the current stream may still use what its own pool
+    hands out."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _run(fn, packed, stream, idx, what):
@@ -189,18 +206,18 @@ def rocs_rope_table(max_pos, rot, base=10000.0, device="cuda", stream=None):
     position ``p`` (angles in 64 bits)."""
     if max_pos < 0 or rot <= 0:
         raise RocsError(1, "rocs_rope_table: max_pos >= 0 and rot > 0")
-    table = torch.empty((int(max_pos), int(rot)), dtype=torch.float32, device=device)
+    table = _empty(stream, (int(max_pos), int(rot)), torch.float32, device)
     _on(table, "device", _fill_rope, (table, base, stream))
     _hold(stream, table)
     return table
 
 
-def _side(x, out, pos, gamma, beta, rope, what, idx, dtype, dh):
+def _side(x, out, pos, gamma, beta, rope, what, idx, dtype, dh, stream):
     if x is None:
         return _NO_SIDE, None
     x_ptr, ld_x = _rows(x, dtype, what, idx, None, dh)
     if out is None:
-        out = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=dtype, device=x.device)
+        out = torch.empty_like(x) if stream is None and x.is_contiguous() else _empty(stream, x.shape, dtype, x.device)
     elif out.shape != x.shape:
         raise RocsError(1, f"{what}_out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
     out_ptr, ld_out = _rows(out, dtype, what + "_out", idx)
@@ -245,9 +262,9 @@ def _norm_rope(idx, x, q, k, pos_q, pos_k, rope, norm, gamma_q, gamma_k, beta_q,
     if dtype not in _DTYPES or x.dim() != 3:
         raise RocsError(1, "q and k must be [tokens, heads, dh] of bf16 or fp32")
     dh = x.shape[2]
-    sq, q_out = _side(q, q_out, pos_q, gamma_q, beta_q, rope, "q", idx, dtype, dh)
-    sk, k_out = _side(k, k_out, pos_k, gamma_k, beta_k, rope, "k", idx, dtype, dh)
-    ws = _ws(256, x.device, idx, workspace)
+    sq, q_out = _side(q, q_out, pos_q, gamma_q, beta_q, rope, "q", idx, dtype, dh, stream)
+    sk, k_out = _side(k, k_out, pos_k, gamma_k, beta_k, rope, "k", idx, dtype, dh, stream)
+    ws = _ws(256, x.device, idx, workspace, stream)
     _run(_lib().rocs_qk_norm_rope_forward,
          _PACK_NORM.pack(*sq, *sk, dh, _DTYPES[dtype], NORMS[norm] if isinstance(norm, str) else int(norm), eps, *_rope(rope, idx),
                          1 if interleaved else 0, ws.data_ptr(), ws.nbytes), stream, idx, "rocs_qk_norm_rope_forward")
@@ -312,7 +329,7 @@ def _append(idx, cache, k, v, tok_off, base, page_table, rope, pos, interleaved,
     if k.dtype not in _DTYPES:
         raise RocsError(1, "k and v must be bf16 or fp32")
     csr = _csr(tok_off, k.device, idx, "tok_off")
-    ws = _ws(256, k.device, idx, workspace)
+    ws = _ws(256, k.device, idx, workspace, stream)
     _move(_lib().rocs_cache_append, "rocs_cache_append", idx, _cache(cache, idx), csr, k, v, base, page_table, rope, pos, interleaved,
           k.dtype, ws, stream)
     _hold(stream, ws, csr[0])
@@ -331,10 +348,10 @@ def _read(idx, cache, tok_off, base, page_table, k, v, workspace, stream):
     csr = _csr(tok_off, dev, idx, "tok_off")
     c = _cache(cache, idx)
     if k is None:
-        k = torch.empty((csr[5], c[6], c[7]), dtype=torch.bfloat16, device=dev)
+        k = _empty(stream, (csr[5], c[6], c[7]), torch.bfloat16, dev)
     if v is None:
-        v = torch.empty_like(k) if k.is_contiguous() else torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
-    ws = _ws(256, dev, idx, workspace)
+        v = torch.empty_like(k) if stream is None and k.is_contiguous() else _empty(stream, k.shape, torch.bfloat16, dev)
+    ws = _ws(256, dev, idx, workspace, stream)
     _move(_lib().rocs_cache_read, "rocs_cache_read", idx, c, csr, k, v, base, page_table, None, None, False, torch.bfloat16, ws, stream)
     _hold(stream, ws, csr[0], k, v)
     rocs_cache_read.last_workspace = ws
@@ -358,11 +375,11 @@ def _dca_cache(idx, q_t, cache, page_table, seq_len, cand_off, q_tokens, scale, 
     if n != C * q_tokens:
         raise RocsError(1, f"q has {n} tokens, cand_off counts {C} candidates of {q_tokens}")
     if o is None:
-        o = torch.empty_like(q_t) if q_t.is_contiguous() else torch.empty((n, H, dh), dtype=torch.bfloat16, device=q_t.device)
+        o = torch.empty_like(q_t) if stream is None and q_t.is_contiguous() else _empty(stream, (n, H, dh), torch.bfloat16, q_t.device)
     elif o.shape != q_t.shape:
         raise RocsError(1, f"o has shape {tuple(o.shape)}, expected {(n, H, dh)}")
     if lse is True:
-        lse = torch.empty((n, H), dtype=torch.float32, device=q_t.device)
+        lse = _empty(stream, (n, H), torch.float32, q_t.device)
     elif lse is False:
         lse = None
     lse_ptr = lim_ptr = 0
@@ -378,7 +395,7 @@ def _dca_cache(idx, q_t, cache, page_table, seq_len, cand_off, q_tokens, scale, 
     a = (*c, R, int(q_tokens), H, cols, scale, off_d, off_h, _per_request(seq_len, R, "seq_len", idx), table, lim_ptr, q_ptr, q_ld,
          _ptr(o, torch.bfloat16, "o", idx, 3), lse_ptr)
     nbytes = lib.rocs_dca_cache_workspace_size(_PACK_DCA.pack(*a, 0, 0))
-    ws = _ws(nbytes, q_t.device, idx, workspace)  # 0: refused arguments, the call below says which
+    ws = _ws(nbytes, q_t.device, idx, workspace, stream)  # 0: refused arguments, the call below says which
     _run(lib.rocs_dca_cache_forward, _PACK_DCA.pack(*a, ws.data_ptr(), ws.nbytes), stream, idx, "rocs_dca_cache_forward")
     _hold(stream, ws, off_dev, o, lse)
     rocs_dca_cache_forward.last_workspace = ws

@@ -45,3 +45,88 @@ def test_steps_midway_between_two_bf16_values(ikbo, dh):
     b[0, 0, 1], b[0, 0, 2] = 4800.0, -15.0
     ikbo.rocs_cache_append(cache, b.bfloat16().cuda(), b.bfloat16().cuda(), [0, 1], zero, table)
     assert cache.k_scale[0, 0, 0].tolist() == [322.0, -15.0] and cache.v_scale[0, 0, 0].tolist() == [322.0, -15.0]
+
+
+def late_write(shape, dtype):
+    """A tensor's memory given back while a write to it still waits on the current stream."""
+    t = torch.empty(shape, dtype=dtype, device="cuda")
+    torch.cuda._sleep(30_000_000)
+    t.view(torch.uint8).fill_(255)
+
+
+@pytest.mark.parametrize("op", ["norm_rope", "read", "attend", "attend_workspace", "table"])
+def test_memory_of_another_stream(ikbo, op):
+    """A call on a stream of its own while the current one still writes to memory that it has given back: outputs and
+    workspaces must not come from there."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    T, H, dh = 4096, 4, 128
+    x = torch.randn(T, H, dh, generator=g, device="cuda").bfloat16()
+    cache = ikbo.CacheQ4.empty(T // 64, 64, H, dh)
+    table, zero = torch.arange(T // 64, dtype=torch.int32, device="cuda")[None], torch.zeros(1, dtype=torch.int32, device="cuda")
+    off, coff = ikbo.offsets([0, T]), ikbo.offsets([0, T])
+    ikbo.rocs_cache_append(cache, x, x, off, zero, table)
+    lens = zero + 700
+    o, lse = torch.empty_like(x), torch.empty(T, H, device="cuda")
+    side = torch.cuda.Stream()
+
+    def call(stream):
+        if op == "norm_rope":
+            return ikbo.rocs_qk_norm_rope_forward(x, stream=stream)[:1]
+        if op == "read":
+            return ikbo.rocs_cache_read(cache, off, zero, table, stream=stream)
+        if op == "attend":
+            return ikbo.rocs_dca_cache_forward(x, cache, table, lens, coff, 1, 0.1, stream=stream)
+        if op == "table":
+            return (ikbo.rocs_rope_table(8192, 128, stream=stream),)
+        return ikbo.rocs_dca_cache_forward(x, cache, table, lens, coff, 1, 0.1, o=o, lse=lse, stream=stream)
+
+    want = [t.clone() for t in call(None)]
+    nbytes = ikbo.rocs_dca_cache_forward.last_workspace.numel() if op == "attend_workspace" else None
+    ikbo.rocs_dca_cache_forward.last_workspace = None
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    if op == "attend_workspace":
+        late_write(nbytes, torch.uint8)
+    else:
+        late_write(want[0].shape, want[0].dtype)
+    got = call(side)
+    if op == "attend_workspace":
+        got = [t.clone() for t in got] if side.synchronize() is None else None
+        assert ikbo.rocs_read_status(ikbo.rocs_dca_cache_forward.last_workspace) == (0, 0)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("op", ["norm_rope", "read", "attend"])
+def test_outputs_of_another_stream_read_later(ikbo, op):
+    """Outputs of a call on a stream of its own, read on the current one behind other work and then given back: a second
+    call must not be handed their memory before that."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    T, H, dh = 4096, 4, 128
+    x, y = (torch.randn(T, H, dh, generator=g, device="cuda").bfloat16() for _ in range(2))
+    caches = [ikbo.CacheQ4.empty(T // 64, 64, H, dh) for _ in range(2)]
+    table, zero = torch.arange(T // 64, dtype=torch.int32, device="cuda")[None], torch.zeros(1, dtype=torch.int32, device="cuda")
+    off, lens = ikbo.offsets([0, T]), zero + 300
+    for c, t in zip(caches, (x, y)):
+        ikbo.rocs_cache_append(c, t, t, off, zero, table)
+    side = torch.cuda.Stream()
+
+    def call(i, stream):
+        if op == "norm_rope":
+            return ikbo.rocs_qk_norm_rope_forward((x, y)[i], stream=stream)[0]
+        if op == "read":
+            return ikbo.rocs_cache_read(caches[i], off, zero, table, stream=stream)[0]
+        return ikbo.rocs_dca_cache_forward(x, caches[i], table, lens, off, 1, 0.1, stream=stream)[0]
+
+    want = [call(i, None).clone() for i in range(2)]
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    first = call(0, side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(30_000_000)
+    copy = torch.empty_like(first).copy_(first)
+    del first
+    second = call(1, side)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want[0]) and torch.equal(second, want[1])
