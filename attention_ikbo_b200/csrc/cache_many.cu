@@ -497,8 +497,10 @@ __global__ void __launch_bounds__(kThreadsMany, 1) rocs_cache_many_kernel(const 
                            pair16<3>(cw[k]));
           }
         } else {
-          // a row with values that are not finite: zeros here, and NaN for the rows that see it (in the epilogue)
-          const bool bad = !(fabsf(bf_hi(sc)) + 15.0f * fabsf(bf_lo(sc)) <= 3.38e38f);
+          // a row with values that are not finite: zeros here, and NaN for the rows that see it (in the epilogue).  Its values
+          // lie between the minimum and 15 steps above it; bf16 holds what is below 0x1.ffp127.
+          const float mn = bf_hi(sc), end = fmaf(15.0f, bf_lo(sc), mn);
+          const bool bad = !(fabsf(mn) < 0x1.ffp127f && fabsf(end) < 0x1.ffp127f);
           const unsigned any = __ballot_sync(0xffffffffu, bad);
           if (any) {
             if (lane == 0) atomicMin(const_cast<int*>(&recs[rec].bad), key0 + __ffs(any) - 1);

@@ -566,7 +566,8 @@ ROCS_API int rocs_cache_read(const rocs_cache_move_args* args, rocs_stream_t str
  *                              -inf where a candidate sees no key
  * Scores are exact up to fp32 sums: codes are exact in bf16, steps and minima enter in fp32.  What a
  * masked row of the cache holds does not matter; a visible row that is held as NaN makes the result
- * NaN.  scale >= 0 and finite.  A length outside [0, max_pages * page] is cut to that range, a page
+ * NaN.  O is summed in fp32 before it is normalised, with weights that may reach 2^20 for a key: values
+ * of V near fp32's limit (above 2^108 over the number of keys) may come out infinite or NaN.  scale >= 0 and finite.  A length outside [0, max_pages * page] is cut to that range, a page
  * outside [0, pages) is replaced by page 0, and either sets ROCS_ERR_DEVICE_INDEX.  C*q*H < 2^31.
  * o_ptr and lse_ptr must not overlap q_ptr's rows or each other.  The kernels (one, or one for
  * requests with few rows and one for the others) are chosen by cand_off_host: the offsets on the

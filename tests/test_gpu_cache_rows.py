@@ -47,6 +47,26 @@ def test_steps_midway_between_two_bf16_values(ikbo, dh):
     assert cache.k_scale[0, 0, 0].tolist() == [322.0, -15.0] and cache.v_scale[0, 0, 0].tolist() == [322.0, -15.0]
 
 
+@pytest.mark.parametrize("dh", [64, 128])
+@pytest.mark.parametrize("n", [3, 200])
+def test_large_finite_values(ikbo, n, dh):
+    """A row of V from about -1.2e38 to 1.2e38, which the cache holds as finite values, is no row of NaN: with one key the
+    output is that row.  Each value is off by the roundings of P and V (one each) and of the output: 3 * 2^-8 of the row's
+    largest."""
+    x = torch.linspace(-1.2e38, 1.2e38, dh)[torch.randperm(dh, generator=torch.Generator().manual_seed(1))].view(1, 1, dh)
+    cache = ikbo.CacheQ4.empty(1, 16, 1, dh)
+    for t in cache:
+        t.view(torch.uint8).fill_(255)
+    table, zero = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ikbo.rocs_cache_append(cache, torch.ones(1, 1, dh, device="cuda"), x.cuda(), [0, 1], zero, table)
+    held = ref.values(cache.v_codes.cpu()[0, 0, :1], cache.v_scale.cpu()[0, 0, :1])
+    assert torch.isfinite(held).all()
+    q = torch.randn(n, 1, dh, device="cuda").bfloat16()
+    o, _ = ikbo.rocs_dca_cache_forward(q, cache, table, zero + 1, [0, n], 1, dh ** -0.5)
+    assert torch.isfinite(o).all()
+    assert torch.all((o.cpu().double()[:, 0] - held).abs() <= 3 * 2.0 ** -8 * held.abs().max())
+
+
 def late_write(shape, dtype):
     """A tensor's memory given back while a write to it still waits on the current stream."""
     t = torch.empty(shape, dtype=dtype, device="cuda")
