@@ -37,6 +37,15 @@ Span span(const void* p, int64_t n, int64_t row, int64_t ld, int64_t es) {
   const uintptr_t b = reinterpret_cast<uintptr_t>(p);
   return {b, b + (uintptr_t)(((n - 1) * ld + row) * es)};
 }
+inline bool apart(const Span& a, const Span& b) { return a.hi <= b.lo || b.hi <= a.lo; }
+// the same for rows of row_a and row_b bytes: also where they lie side by side in one wider buffer, ld bytes a row
+bool rows_apart(const Span& a, int64_t row_a, int64_t ld_a, const Span& b, int64_t row_b, int64_t ld_b) {
+  if (apart(a, b)) return true;
+  if (ld_a != ld_b) return false;
+  const int64_t d = (int64_t)(b.lo > a.lo ? b.lo - a.lo : a.lo - b.lo) % ld_a;
+  const int64_t first = b.lo > a.lo ? row_a : row_b, second = b.lo > a.lo ? row_b : row_a;
+  return d >= first && d + second <= ld_a;
+}
 
 int side_validate(const rocs_norm_rope_side& s, const rocs_norm_rope_args* a) {
   if (s.n < 0 || s.heads < 0) return ROCS_ERR_INVALID_ARG;
@@ -67,14 +76,7 @@ int overlap_validate(const rocs_norm_rope_args* a) {
       const int64_t rowt = t->heads * a->dh, ldt = (i < 2 ? t->ld_x : t->ld_out) ? (i < 2 ? t->ld_x : t->ld_out) : rowt;
       const void* pt = i < 2 ? t->x : t->out;
       if (i < 2 && (i & 1) == o && pt == s[o]->out && ldt == ldo) continue;
-      const Span q = span(pt, t->n, rowt, ldt, es);
-      if (out.hi <= q.lo || q.hi <= out.lo) continue;
-      // rows of one wider buffer side by side: same stride, columns apart
-      if (ldt == ldo) {
-        const int64_t ldb = ldo * es, d = (int64_t)(q.lo > out.lo ? q.lo - out.lo : out.lo - q.lo) % ldb;
-        const int64_t first = q.lo > out.lo ? row * es : rowt * es, second = q.lo > out.lo ? rowt * es : row * es;
-        if (d >= first && d + second <= ldb) continue;
-      }
+      if (rows_apart(out, row * es, ldo * es, span(pt, t->n, rowt, ldt, es), rowt * es, ldt * es)) continue;
       return ROCS_ERR_INVALID_ARG;
     }
   }
@@ -102,6 +104,14 @@ int cache_validate(const rocs_cache_q4& c) {
   for (const void* p : ptrs)
     if ((c.pages > 0 && !p) || !al(p, 16)) return ROCS_ERR_INVALID_ARG;
   return ROCS_OK;
+}
+// the cache's four buffers
+void cache_spans(const rocs_cache_q4& c, Span (&s)[4]) {
+  const int64_t rows = c.pages * c.heads * c.page;
+  s[0] = span(c.k_codes, 1, rows, rows, c.dh / 2);
+  s[1] = span(c.v_codes, 1, rows, rows, c.dh / 2);
+  s[2] = span(c.k_scale, 1, rows, rows, 4);
+  s[3] = span(c.v_scale, 1, rows, rows, 4);
 }
 CacheQ4 cache_of(const rocs_cache_q4& c) {
   CacheQ4 q;
@@ -136,10 +146,27 @@ int move_validate(const rocs_cache_move_args* a, bool append, int64_t* T) {
   return append ? rope_validate(a->rope, a->max_pos, a->rot, a->cache.dh) : ROCS_OK;
 }
 
+// What a call writes must not overlap what it reads or writes elsewhere: append the cache's buffers, read k and v.
+int move_overlap_validate(const rocs_cache_move_args* a, bool append, int64_t T) {
+  if (T == 0) return ROCS_OK;
+  const int64_t row = a->cache.heads * a->cache.dh, es = a->dtype == ROCS_BF16 ? 2 : 4;
+  const int64_t ld[2] = {a->k_ld ? a->k_ld : row, a->v_ld ? a->v_ld : row};
+  const Span x[2] = {span(a->k, T, row, ld[0], es), span(a->v, T, row, ld[1], es)};
+  Span c[4];
+  cache_spans(a->cache, c);
+  for (int i = 0; i < 4; ++i) {
+    if (!apart(x[0], c[i]) || !apart(x[1], c[i])) return ROCS_ERR_INVALID_ARG;
+    for (int j = 0; j < i && append; ++j)
+      if (!apart(c[i], c[j])) return ROCS_ERR_INVALID_ARG;
+  }
+  return append || rows_apart(x[0], row * es, ld[0] * es, x[1], row * es, ld[1] * es) ? ROCS_OK : ROCS_ERR_INVALID_ARG;
+}
+
 int cache_move(const rocs_cache_move_args* a, bool append, cudaStream_t st) {
   int64_t T = 0;
   int rc = move_validate(a, append, &T);
-  if (rc || (rc = workspace_validate(a->workspace, a->workspace_bytes, sizeof(WsHeader)))) return rc;
+  if (rc || (rc = workspace_validate(a->workspace, a->workspace_bytes, sizeof(WsHeader))) || (rc = move_overlap_validate(a, append, T)))
+    return rc;
   CacheMoveParams p;
   std::memset(&p, 0, sizeof(p));
   p.c = cache_of(a->cache);
@@ -215,14 +242,15 @@ int attn_validate(const rocs_dca_cache_args* a, AttnPlan* pl) {
     const int64_t row = a->H * a->cache.dh;
     if (a->q_ld != 0 && a->q_ld < row) return ROCS_ERR_INVALID_ARG;
     if (a->q_ld % 8 || a->q_ld >= (int64_t(1) << 31)) return ROCS_ERR_UNSUPPORTED;
-    // outputs that overlap the queries or each other: queries are read again after other parts' outputs are written
+    // outputs that overlap the queries, the cache or each other: all are read after other parts' outputs are written
     const int64_t n = pl->C * a->q;
     const Span q = span(a->q_ptr, n, row, a->q_ld ? a->q_ld : row, 2), o = span(a->o_ptr, n, row, row, 2);
-    if (q.lo < o.hi && o.lo < q.hi) return ROCS_ERR_INVALID_ARG;
-    if (a->lse_ptr) {
-      const Span l = span(a->lse_ptr, n, a->H, a->H, 4);
-      if ((l.lo < q.hi && q.lo < l.hi) || (l.lo < o.hi && o.lo < l.hi)) return ROCS_ERR_INVALID_ARG;
-    }
+    const Span l = a->lse_ptr ? span(a->lse_ptr, n, a->H, a->H, 4) : Span{0, 0};
+    Span c[4];
+    cache_spans(a->cache, c);
+    if (!apart(q, o) || !apart(q, l) || !apart(o, l)) return ROCS_ERR_INVALID_ARG;
+    for (const Span& b : c)
+      if (!apart(o, b) || !apart(l, b)) return ROCS_ERR_INVALID_ARG;
     const int64_t G = a->H / a->cache.heads;
     const bool wide = a->cache.dh == 128;
     const int64_t limit = wide ? kFewLimit128 : kFewLimit64, many = wide ? kManyCost128 : kManyCost64;

@@ -528,6 +528,8 @@ typedef struct {
  * rocs_cache_read: the reverse, rows of the cache as bf16 values (rounded once) in k, v (outputs; dtype
  * must be ROCS_BF16; rope and pos are ignored): what rocs_dca_forward reads.  A token whose place is
  * bad reads as zeros and sets ROCS_ERR_DEVICE_INDEX.
+ * k and v must not overlap the cache; append: nor its four buffers each other; read: nor k and v each
+ * other (rows side by side in one wider buffer, of one stride, are fine): ROCS_ERR_INVALID_ARG.
  * Workspace: 256 bytes.  One kernel launch each. */
 typedef struct {
   rocs_cache_q4 cache;
@@ -567,9 +569,10 @@ ROCS_API int rocs_cache_read(const rocs_cache_move_args* args, rocs_stream_t str
  * Scores are exact up to fp32 sums: codes are exact in bf16, steps and minima enter in fp32.  What a
  * masked row of the cache holds does not matter; a visible row that is held as NaN makes the result
  * NaN.  O is summed in fp32 before it is normalised, with weights that may reach 2^20 for a key: values
- * of V near fp32's limit (above 2^108 over the number of keys) may come out infinite or NaN.  scale >= 0 and finite.  A length outside [0, max_pages * page] is cut to that range, a page
- * outside [0, pages) is replaced by page 0, and either sets ROCS_ERR_DEVICE_INDEX.  C*q*H < 2^31.
- * o_ptr and lse_ptr must not overlap q_ptr's rows or each other.  The kernels (one, or one for
+ * of V near fp32's limit (above 2^108 over the number of keys) may come out infinite or NaN.
+ * scale >= 0 and finite.  A length outside [0, max_pages * page] is cut to that range, a page outside
+ * [0, pages) is replaced by page 0, and either sets ROCS_ERR_DEVICE_INDEX.  C*q*H < 2^31.
+ * o_ptr and lse_ptr must not overlap q_ptr's rows, the cache or each other.  The kernels (one, or one for
  * requests with few rows and one for the others) are chosen by cand_off_host: the offsets on the
  * device must be the same, in replays of a captured call too.
  * The workspace size depends on the current device's SM count. */
