@@ -3,7 +3,9 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
+import threading
 
 import numpy as np
 import torch
@@ -149,12 +151,40 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+_call = threading.local()  # .stream: the stream that the running call was given, or None
+
+
+def _empty(shape, dtype, device):
+    """Memory that a call makes: from the pool of the stream that it was given, since the current stream may still use
+    what its own pool hands out; it may then be used on both."""
+    stream = getattr(_call, "stream", None)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _on_tensor_device(fn):
     """Run ``fn`` with the device of its first CUDA tensor argument current (else the ``device``
     keyword's, else the current device), so that the library's per-device state (SM count, kernel
-    attributes, the no-alloc scratch array) and the default stream belong to the device the data is on."""
+    attributes, the no-alloc scratch array) and the default stream belong to the device the data is on.
+    With ``stream``, memory made on the way is that stream's."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
     @functools.wraps(fn)
     def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return on_device(args, kw)
+        before, _call.stream = getattr(_call, "stream", None), stream
+        try:
+            return on_device(args, kw)
+        finally:
+            _call.stream = before
+
+    def on_device(args, kw):
         for t in list(args) + list(kw.values()):
             if isinstance(t, torch.Tensor) and t.is_cuda:
                 with torch.cuda.device(t.device):
@@ -185,6 +215,9 @@ def _offsets(off, device):
     else:
         host = np.ascontiguousarray(np.asarray(off, dtype=np.int32))
         dev = torch.from_numpy(host).to(device)
+    stream = getattr(_call, "stream", None)
+    if stream is not None and dev.is_cuda:  # made on the current stream, read on the call's
+        dev.record_stream(stream)
     return dev, host
 
 
@@ -198,7 +231,7 @@ def _workspace(nbytes, device, given):
         if given.numel() * given.element_size() < nbytes:
             raise RocsError(6, "workspace")
         return given
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    return _empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
 def _lcb_args(x_req, x_cand, w_rr, w_cr, w_cc, cand_off, y_req, y_cand):
@@ -209,9 +242,9 @@ def _lcb_args(x_req, x_cand, w_rr, w_cr, w_cc, cand_off, y_req, y_cand):
     C = int(off_h[-1])
     n_c, o_r, o_c = x_cand.shape[1] if x_cand.dim() == 3 else w_cc.shape[1], w_rr.shape[0], w_cc.shape[0]
     if y_req is None:
-        y_req = torch.empty((R, o_r, d), dtype=x_req.dtype, device=dev)
+        y_req = _empty((R, o_r, d), dtype=x_req.dtype, device=dev)
     if y_cand is None:
-        y_cand = torch.empty((C, o_c, d), dtype=x_req.dtype, device=dev)
+        y_cand = _empty((C, o_c, d), dtype=x_req.dtype, device=dev)
     for t in (x_req, x_cand, w_rr, w_cr, w_cc, y_req, y_cand):
         if not (t.is_cuda and t.is_contiguous() and t.dtype == x_req.dtype):
             raise RocsError(1, "LCB tensors must be contiguous CUDA tensors of one dtype")
@@ -362,9 +395,9 @@ def _dca_args(q_t, k_t, v_t, cand_off, seq_off, q_tokens, scale, o, lse):
     R = len(co_h) - 1
     H, dh = k_t.shape[1], k_t.shape[2]
     if o is None:
-        o = torch.empty(q_t.shape, dtype=torch.bfloat16, device=dev)
+        o = _empty(q_t.shape, dtype=torch.bfloat16, device=dev)
     if lse is True:
-        lse = torch.empty(q_t.shape[:2], dtype=torch.float32, device=dev)
+        lse = _empty(q_t.shape[:2], dtype=torch.float32, device=dev)
     elif lse is False:
         lse = None
     for t in (q_t, k_t, v_t, o):
@@ -421,10 +454,10 @@ def rocs_dca_block_forward(s_seq, w_kv, q_c, q_r, cand_off, seq_off, q_tokens, q
     so_d, so_h = _offsets(seq_off, dev)
     R = len(co_h) - 1
     H, dh = q_c.shape[1], q_c.shape[2]
-    o_c = torch.empty(q_c.shape, dtype=torch.bfloat16, device=dev) if o_c is None else o_c
-    o_r = torch.empty(q_r.shape, dtype=torch.bfloat16, device=dev) if o_r is None else o_r
-    lse_c = torch.empty(q_c.shape[:2], dtype=torch.float32, device=dev) if lse else None
-    lse_r = torch.empty(q_r.shape[:2], dtype=torch.float32, device=dev) if lse else None
+    o_c = _empty(q_c.shape, dtype=torch.bfloat16, device=dev) if o_c is None else o_c
+    o_r = _empty(q_r.shape, dtype=torch.bfloat16, device=dev) if o_r is None else o_r
+    lse_c = _empty(q_c.shape[:2], dtype=torch.float32, device=dev) if lse else None
+    lse_r = _empty(q_r.shape[:2], dtype=torch.float32, device=dev) if lse else None
     for t in (s_seq, w_kv, q_c, q_r, o_c, o_r):
         if not (t.is_cuda and t.is_contiguous() and t.dtype == torch.bfloat16):
             raise RocsError(1, "DCA block tensors must be contiguous bf16 CUDA tensors")
@@ -452,7 +485,7 @@ def rocs_proj_forward(inp, w, out=None, workspace=None, stream=None):
     M, K = inp.shape[0], int(np.prod(inp.shape[1:]))
     N = w.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=inp.device)
+        out = _empty((M, N), dtype=torch.bfloat16, device=inp.device)
     for t in (inp, w, out):
         if not (t.is_cuda and t.is_contiguous() and t.dtype == torch.bfloat16):
             raise RocsError(1, "projection tensors must be contiguous bf16 CUDA tensors")
@@ -505,7 +538,7 @@ def rocs_pad_cols(src, ld_dst, dst=None, stream=None):
     cols = min(src.shape[-1], ld_dst)
     rows = src.numel() // src.shape[-1] if src.numel() else 0
     if dst is None:
-        dst = torch.empty(tuple(src.shape[:-1]) + (ld_dst,), dtype=src.dtype, device=src.device)
+        dst = _empty(tuple(src.shape[:-1]) + (ld_dst,), dtype=src.dtype, device=src.device)
     _check(lib.rocs_pad_cols(_ptr(src), rows, cols, src.shape[-1], _ptr(dst), ld_dst, src.element_size(),
                              _stream(stream)), "rocs_pad_cols")
     return dst
@@ -525,9 +558,9 @@ def rocs_fm_forward(x_req, x_cand, cand_off, y_req=None, y_cand=None, ld_req=0, 
     ld_r = ld_req or rocs_align_cols(n_r, 2)
     ld_c = ld_cand or rocs_align_cols(n_r + n_c, 2)
     if y_req is None:
-        y_req = torch.empty((R, n_r, ld_r), dtype=torch.bfloat16, device=dev)
+        y_req = _empty((R, n_r, ld_r), dtype=torch.bfloat16, device=dev)
     if y_cand is None:
-        y_cand = torch.empty((C, n_c, ld_c), dtype=torch.bfloat16, device=dev)
+        y_cand = _empty((C, n_c, ld_c), dtype=torch.bfloat16, device=dev)
     for t in (x_req, x_cand, y_req, y_cand):
         if not (t.is_cuda and t.is_contiguous() and t.dtype == torch.bfloat16):
             raise RocsError(1, "FM tensors must be contiguous CUDA bf16 tensors")
@@ -552,8 +585,8 @@ def rocs_chain_prepare_weights(w_q, w_rr, w_cr, w_cc, d, stream=None):
         if not (t.is_cuda and t.is_contiguous() and t.dtype == torch.bfloat16):
             raise RocsError(1, "chain weights must be contiguous CUDA bf16 tensors")
     n_out, (o_r, n_r), (o_c, n_c) = w_q.shape[0], w_rr.shape, w_cc.shape
-    w_fold = torch.empty((n_out, n_c * d), dtype=torch.bfloat16, device=w_q.device)
-    w_rs = torch.empty((o_r + o_c, n_r), dtype=torch.bfloat16, device=w_q.device)
+    w_fold = _empty((n_out, n_c * d), dtype=torch.bfloat16, device=w_q.device)
+    w_rs = _empty((o_r + o_c, n_r), dtype=torch.bfloat16, device=w_q.device)
     a = ChainWeightsArgs(n_out=n_out, o_r=o_r, o_c=o_c, n_r=n_r, n_c=n_c, d=d, w_q=w_q.data_ptr(),
                          w_rr=w_rr.data_ptr(), w_cr=w_cr.data_ptr(), w_cc=w_cc.data_ptr(), w_fold=w_fold.data_ptr(),
                          w_rs=w_rs.data_ptr())
@@ -574,9 +607,9 @@ def rocs_chain_split_forward(x_req, x_cand, w_rs, w_q, w_fold, cand_off, o_r, y_
     o_c = w_rs.shape[0] - o_r
     n_out = w_q.shape[0]
     if y_req is None:
-        y_req = torch.empty((R, o_r + o_c, d), dtype=torch.bfloat16, device=dev)
+        y_req = _empty((R, o_r + o_c, d), dtype=torch.bfloat16, device=dev)
     if q is None:
-        q = torch.empty((C, n_out), dtype=torch.bfloat16, device=dev)
+        q = _empty((C, n_out), dtype=torch.bfloat16, device=dev)
     for t in (x_req, x_cand, w_rs, w_q, w_fold, y_req, q):
         if not (t.is_cuda and t.is_contiguous() and t.dtype == torch.bfloat16):
             raise RocsError(1, "split chain tensors must be contiguous CUDA bf16 tensors")
