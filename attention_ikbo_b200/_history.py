@@ -321,7 +321,8 @@ def rocs_cache_append(cache, k, v, tok_off, base, page_table, rope=None, pos=Non
                       stream=None):
     """Append ``k``, ``v`` [T, heads, dh] (bf16 or fp32) to the histories of a :class:`CacheQ4`: token ``i`` of request
     ``r`` (row ``tok_off[r] + i``) goes to slot ``base[r] + i``, keys rotated by ``pos`` (default: the slot) on the way.
-    ``base`` [R] int32 is not changed.  Returns ``cache``."""
+    ``base`` [R] int32 is not changed.  Tokens may lie apart: the halves of a stacked K/V projection
+    (:func:`rocs_proj_forward` of a request's sequence) go in as they are.  Returns ``cache``."""
     return _on(k, "k", _append, (cache, k, v, tok_off, base, page_table, rope, pos, interleaved, workspace, stream))
 
 
