@@ -25,7 +25,7 @@
 // their use.  setmaxnreg moves registers to the softmax warps.
 // Work is shared out by cache_work.cuh: equal runs of blocks, partial results merged by the last to finish.
 //
-// What bounds it is what runs beside the tensor work (880-910 us for the case above, 0.55 of the bf16 rate; 202 us for 512
+// What bounds it is what runs beside the tensor work (870-910 us for the case above, 0.55 of the bf16 rate; 205 us for 512
 // candidates to each of 32 histories of 2048 keys with 8 heads): S products read all the shared-memory bandwidth there is
 // and go first, so a block's conversion, some 200 instructions a warp, takes 1500 cycles, and the roles' code together does
 // not fit the instruction cache, which is why conversion loops are rolled (unrolled: 1127 us) and load one row ahead.

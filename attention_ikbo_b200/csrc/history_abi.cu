@@ -202,8 +202,10 @@ int cache_move(const rocs_cache_move_args* a, bool append, cudaStream_t st) {
 
 // ---------------------------------------------------------------- attention over the cache
 // Which kernel takes which request is chosen by what their units cost, as measured with equal histories (32 of 4096 keys, 8
-// heads): the kernel for few rows takes 66 us (dh = 64: 41) for every 16 rows of the key heads, the one for many 155 (140)
-// for up to 256, so up to 32 (48) rows are as well off with the first.  Calls of a single kind get one kernel; calls with
+// heads): the kernel for few rows takes 66 us (dh = 64: 41) for every 16 rows of the key heads, the one for many 150 (134)
+// for up to 128 and 183 (149) for 256, so up to 32 (48) rows are about as well off with the first.  At that border the two
+// took 156 and 150 us (141 and 134); with 8 histories of 16384 keys 154 and 143 (139 and 120), with 256 of 512 keys 191 and
+// 182 (182 and 157).  Calls of a single kind get one kernel; calls with
 // both kinds get both kernels, one after the other, only where that saves a fifth, because each ends in a tail of its own
 // (16 requests of 16-64 rows of 64: 35 us with the first alone, 46 with the second alone, 62 with both).
 constexpr int kFewCost = 10, kManyCost128 = 24, kManyCost64 = 34;

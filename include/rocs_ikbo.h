@@ -566,7 +566,9 @@ ROCS_API int rocs_cache_read(const rocs_cache_move_args* args, rocs_stream_t str
  *                              only; a limit above its length means all, one below 1 none
  *   o_ptr  [C*q, H, dh] bf16, lse_ptr [C*q, H] fp32 or NULL: as in rocs_dca_forward; O = 0 and LSE =
  *                              -inf where a candidate sees no key
- * Scores are exact up to fp32 sums: codes are exact in bf16, steps and minima enter in fp32.  What a
+ * Scores are exact up to fp32 sums: codes are exact in bf16, steps and minima enter in fp32.  For
+ * requests with few rows O carries no other rounding than its own; for those with many the weights and
+ * V are rounded to bf16 once each, as in rocs_dca_forward.  Neither error grows with the history.  What a
  * masked row of the cache holds does not matter; a visible row that is held as NaN makes the result
  * NaN.  O is summed in fp32 before it is normalised, with weights that may reach 2^20 for a key: values
  * of V near fp32's limit (above 2^108 over the number of keys) may come out infinite or NaN.
