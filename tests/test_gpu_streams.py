@@ -36,11 +36,23 @@ def make(ikbo, op, seed):
     if op == "proj":
         x, w = r(4096, 512), r(512, 512) / 16
         return lambda stream: (ikbo.rocs_proj_forward(x, w, stream=stream),)
+    if op == "cache":
+        k, v, q, tok = r(1200, 4, d), r(1200, 4, d), r(4096, 4, d), ikbo.offsets([0, 300, 500, 900, 1200])
+        cache, cand = ikbo.CacheQ4.empty(28, 64, 4, d), ikbo.offsets([0, 1000, 2000, 2000, 4096])
+        table = torch.arange(28, dtype=torch.int32, device="cuda").view(4, 7)
+        zero, lens = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.tensor([300, 200, 400, 300], dtype=torch.int32, device="cuda")
+
+        def call(stream):
+            ikbo.rocs_cache_append(cache, k, v, tok, zero, table, stream=stream)
+            x, _ = ikbo.rocs_qk_norm_rope_forward(q, stream=stream)
+            return ikbo.rocs_dca_cache_forward(x, cache, table, lens, cand, 1, 0.1, stream=stream)
+
+        return call
     x = r(4096, 500)
     return lambda stream: (ikbo.rocs_pad_cols(x, 512, stream=stream),)
 
 
-OPS = ["lcb", "fm", "dca", "proj", "pad_cols"]
+OPS = ["lcb", "fm", "dca", "proj", "cache", "pad_cols"]
 
 
 @pytest.mark.parametrize("op", OPS)
@@ -72,3 +84,27 @@ def test_outputs_read_later_and_given_back(ikbo, op):
     second = calls[1](side)[0]
     torch.cuda.synchronize()
     assert torch.equal(copy, want[0]) and torch.equal(second, want[1])
+
+
+@pytest.mark.parametrize("op", OPS)
+def test_captured_on_a_forked_stream(ikbo, op):
+    """A capture whose call is given the capturing stream, and one that forks a stream of its own for it."""
+    call = make(ikbo, op, 1)
+    want = [t.clone() for t in call(None)]
+    for fork in (False, True):
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            here = torch.cuda.current_stream()
+            if fork:
+                side.wait_stream(here)
+                got = call(side)
+                here.wait_stream(side)
+            else:
+                got = call(here)
+        for _ in range(2):
+            for t in got:
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
